@@ -367,8 +367,9 @@ def _exact_quantize(s):
     v = w.view(n, k // size, size)
     top = v.abs().max(2).values
     if fmt == "mx4":
-        scale = torch.exp2(torch.floor(torch.log2(top)) - 2).clamp(
-            2.0 ** -127, 2.0 ** 125)
+        e = torch.floor(torch.log2(top))  # may be one off next to a power
+        e = e + (torch.exp2(e + 1) <= top) - (torch.exp2(e) > top)
+        scale = torch.exp2(e - 2).clamp(2.0 ** -127, 2.0 ** 125)
         unit = scale
     else:
         g = s["g"]
