@@ -1,7 +1,7 @@
 /*
- * tq.h — packed ternary weight matmul for NVIDIA B200 (sm_100a): C ABI.
+ * tq.h — packed low-bit weight matmul for NVIDIA B200 (sm_100a): C ABI.
  *
- * Two weight formats:
+ * Two ternary weight formats, and two of 4-bit floats (below):
  *
  *   TQ_FMT_A  group ternary ("Does your weight format deserve a kernel?",
  *             precisit.com). A group of G consecutive weights of a row shares
@@ -27,6 +27,17 @@
  *             accumulator (sections 3.3 and 4.2). The decoded weight is
  *             w = rho[n / rows_per_scale] * LUT[code] (rho = 1 when absent).
  *
+ *   TQ_FMT_MX4, TQ_FMT_NV4
+ *             4-bit floats with a scale per block of consecutive weights of a
+ *             row. Both store E2M1 codes (sign, two exponent bits, one
+ *             mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives).
+ *             MX4 (MXFP4 of "OCP Microscaling Formats (MX) Specification",
+ *             v1.0, sections 5 and 6): blocks of 32, one E8M0 byte b each,
+ *             w = c 2^(b - 127); b = 255 is NaN.
+ *             NV4: blocks of 16, one E4M3 byte each (value s >= 0, sign bit
+ *             clear, 0x7F is NaN) and one fp32 tensor scale g, w = c s g.
+ *             4.25 and 4.5 bits per weight.
+ *
  * Layouts (all row-major, C order):
  *   W      bf16 [n][k], contiguous.
  *   A      codes  uint8  [planes][n][k/G][ceil(G/5)]  (plane p starts at
@@ -40,6 +51,10 @@
  *          lut    fp32   [128]: LUT7[i] = LUT[used[i]] (tq_build_lut7);
  *          rho as B (alphaneural.io page, section 8.1, the 7-bit truncated
  *          alphabet: a layer that uses at most 128 of the 243 words)
+ *   MX4    codes  uint8  [n][k/2]: code of column 2j in the low four bits of
+ *   NV4           byte j, of column 2j + 1 in the high four;
+ *          scales uint8  [n][k/32] (MX4) or [n][k/16] (NV4);
+ *          lut    NV4: fp32 [1], the tensor scale g (NULL: g = 1); k % 32 == 0
  *   x      bf16 [batch][ldx];  y fp32 [batch][ldy];  y = x * W_hat^T.
  *
  * Conventions:
@@ -98,8 +113,15 @@ typedef enum {
 typedef enum {
   TQ_FMT_A = 1, /* group ternary, 5 trits per byte, fp16 group scales */
   TQ_FMT_B = 2, /* 243-entry ladder code book, one code per byte */
-  TQ_FMT_B7 = 3 /* Format B over a used-code table: 7-bit indices */
+  TQ_FMT_B7 = 3, /* Format B over a used-code table: 7-bit indices */
+  TQ_FMT_MX4 = 4, /* E2M1 codes, E8M0 scale per block of 32 */
+  TQ_FMT_NV4 = 5  /* E2M1 codes, E4M3 scale per block of 16, tensor scale */
 } tq_format;
+
+typedef enum {
+  TQ_Y_F32 = 0, /* fp32 output */
+  TQ_Y_BF16 = 1 /* bf16 output, one round-to-nearest-even at the end */
+} tq_y_type;
 
 typedef struct {
   int32_t format;          /* tq_format */
@@ -124,10 +146,15 @@ typedef struct {
                               books of 256 fp32 (one tq_build_lut per
                               block's ladder). A: must be 0 */
 } tq_weights;
+/* TQ_FMT_MX4 / TQ_FMT_NV4 descriptors: codes and scales as laid out above
+ * (scales is a byte pointer stored in this field), both 16-byte aligned;
+ * lut = the device tensor scale g (NV4, 4-byte aligned) or NULL; planes 1;
+ * group 0 or the block size; k_cols % 32 == 0; every other field 0. */
 
 /* Bytes of a package: A = planes * n * (k/G) * (ceil(G/5) + 2) (codes and
  * scales; "Count the bytes you actually wrote"), B = n * k + 972 (codes and
- * the 243-entry table; rho excluded). Returns 0 for invalid arguments.
+ * the 243-entry table; rho excluded), MX4 = n * k/2 + n * k/32, NV4 =
+ * n * k/2 + n * k/16 + 4. Returns 0 for invalid arguments.
  * Host only; no GPU needed. */
 size_t tq_packed_bytes(int32_t format, int64_t n, int64_t k, int32_t group,
                        int32_t planes);
@@ -189,14 +216,48 @@ tq_status tq_encode_b(const void *W_bf16, int64_t n, int64_t k,
                       uint16_t *rho_out, float *alpha_out, int32_t *dev_status,
                       void *cuda_stream);
 
+/* Quantize a bf16 matrix (weights, or the rows of x before tq_linear_f4) to
+ * 4-bit floats with a scale per block. Every decision below is the one exact
+ * arithmetic gives; ties round to the even code.
+ *   MX4 (OCP MX v1.0, section 6.3): b = floor(log2 max|v|) - 2 + 127 over the
+ *       block's 32 values, clamped to 0 .. 252; code = E2M1(v 2^(127 - b)),
+ *       magnitudes above 6 become 6. An all-zero block has b = 0.
+ *   NV4: s = E4M3(max|v| / (6 g)) over the block's 16 values, at most 448;
+ *       code = E2M1(v / (s g)), at most 6; s = 0 gives codes of zero. Without
+ *       a given scale, g = fp32(max|W| / 2688) (1 for an all-zero matrix), so
+ *       that the largest block scale is 448.
+ *   The sign bit of a zero is kept.
+ *   W_bf16        device, bf16 [n][ldw], 16-byte aligned, ldw >= k,
+ *                 ldw % 8 == 0; k % 32 == 0.
+ *   format        TQ_FMT_MX4 or TQ_FMT_NV4.
+ *   codes_out     device, n * k/2 bytes, 16-byte aligned.
+ *   scales_out    device, n * k/32 (MX4) or n * k/16 (NV4) bytes, 16-byte
+ *                 aligned.
+ *   tensor_scale  NV4: device fp32 [1], 4-byte aligned; read when
+ *                 scale_given != 0 (finite and > 0, else TQ_ERR_INVALID_ARG
+ *                 in dev_status and NaN block scales), written otherwise.
+ *                 MX4: NULL, with scale_given 0.
+ *   dev_status    device int32 or NULL: TQ_ERR_NONFINITE for NaN / Inf in W;
+ *                 such a block gets the scale NaN and codes of zero, and the
+ *                 maximum behind g skips its values.
+ * Deterministic. */
+tq_status tq_quantize_f4(const void *W_bf16, int64_t n, int64_t k, int64_t ldw,
+                         int32_t format, uint8_t *codes_out,
+                         uint8_t *scales_out, float *tensor_scale,
+                         int32_t scale_given, int32_t *dev_status,
+                         void *cuda_stream);
+
 /* Decode a package to bf16 (precisit.com page, "Three values and a shared
  * scale": W_hat = bf16(s t); alphaneural.io page, section 3.3).
  *   A: W_hat = bf16_RNE(fp32_RN(s1 t1 [+ s2 t2])).
  *   B: W_hat = bf16_RNE(fp32_RN(rho * LUT[code])), or bf16_RNE(LUT[code]).
+ *   MX4: W_hat = bf16_RNE(c 2^(b - 127)).
+ *   NV4: W_hat = bf16_RNE(fp32_RN((c s) g)).
  *   W_bf16_out  device, bf16 [n][k] contiguous, 16-byte aligned.
  *   dev_status  device int32 or NULL: TQ_ERR_BAD_CODE for a byte >= 243 or a
  *               Format A padding digit != 1 (the value written there is
- *               unspecified). */
+ *               unspecified), and for an NV4 scale byte with its sign bit
+ *               set (read without it). NaN scales give NaN. */
 tq_status tq_unpack(const tq_weights *w, void *W_bf16_out, int32_t *dev_status,
                     void *cuda_stream);
 
@@ -205,6 +266,7 @@ tq_status tq_unpack(const tq_weights *w, void *W_bf16_out, int32_t *dev_status,
  * inside a matrix multiplication; alphaneural.io page, section 4.2).
  *   A: y[b][n] = sum_p sum_g s_p[n][g] sum_{j in g} t_p[n][j] x[b][j]
  *   B: y[b][n] = rho[n / rows_per_scale] * sum_k LUT[code[n][k]] x[b][k]
+ *   MX4, NV4: y[b][n] = [g] sum_k c[n][k] scale[n][k / block] x[b][k]
  *   x     device, bf16 [batch][ldx], 16-byte aligned, ldx >= k, ldx % 8 == 0.
  *   y     device, fp32 [batch][ldy], 4-byte aligned, ldy >= n.
  *         Overwritten. fp32 accumulation.
@@ -263,6 +325,34 @@ tq_status tq_linear_experts(const tq_experts *w, const int32_t *ids,
                             int64_t n_tokens, const void *x_bf16, int64_t ldx,
                             float *y, int64_t ldy, int32_t *dev_status,
                             void *cuda_stream);
+
+/* Product of two 4-bit matrices of one format:
+ *   y[b][n] = g_w g_x sum_k c_w[n][k] s_w[n][k / block]
+ *                          c_x[b][k] s_x[b][k / block]
+ * (g = 1 for MX4). x is described as weights are: x->n_rows = batch rows,
+ * x->k_cols = w->k_cols (tq_quantize_f4 makes it from bf16 rows).
+ *   y       device, fp32 or bf16 [batch][ldy] by y_type (tq_y_type), 4-byte
+ *           aligned (fp32) or 2-byte aligned (bf16), ldy >= n. Overwritten;
+ *           fp32 accumulation.
+ * TQ_ERR_SHAPE when the columns differ, TQ_ERR_INVALID_ARG when the formats
+ * do or are not 4-bit ones. A NaN block scale gives NaN in its row (w) or
+ * batch row (x). Zero rows on either side: nothing to do. Deterministic. */
+tq_status tq_linear_f4(const tq_weights *w, const tq_weights *x, void *y,
+                       int64_t ldy, int32_t y_type, void *cuda_stream);
+
+/* Expert-indexed product with 4-bit weights:
+ *   y[t][n] = sum_k w_{ids[t]}[n][k] x[t][k],  t = 0 .. n_tokens - 1.
+ *   w         one expert's shape (n_rows, k_cols), the pointers of expert 0;
+ *             expert e lies behind it at codes + e * n * k/2, scales +
+ *             e * n * k/32 (MX4) or k/16 (NV4), and lut + e (one tensor scale
+ *             per expert) when lut is not NULL. Formats MX4 and NV4.
+ *   n_experts 1 .. 65535.
+ *   ids, x, y, n_tokens, dev_status: as for tq_linear_experts. */
+tq_status tq_linear_experts_f4(const tq_weights *w, int32_t n_experts,
+                               const int32_t *ids, int64_t n_tokens,
+                               const void *x_bf16, int64_t ldx, float *y,
+                               int64_t ldy, int32_t *dev_status,
+                               void *cuda_stream);
 
 /* 7-bit truncated alphabet (alphaneural.io page, section 8.1): turn Format B
  * codes [n][k] (k % 16 == 0) into the layer's table of used codes and 7-bit

@@ -5,6 +5,7 @@
 #include <string.h>
 
 #include "tq_common.cuh"
+#include "tq_f4.cuh"
 #include "tq_linear.cuh"
 #include "tq_testing.h"
 
@@ -79,6 +80,19 @@ tq_status check_weights(const tq_weights *w, tq::WeightsView *v) {
     if (w->scales != nullptr && !aligned(w->scales, 2)) return TQ_ERR_ALIGNMENT;
     v->group = 0;
     if (w->rows_per_scale == 0) v->scales = nullptr;
+  } else if (tq::is_f4(w->format)) {
+    const int block = tq::f4_block(w->format);
+    if (w->planes != 1 || w->lut_rows != 0 || w->rows_per_scale != 0 ||
+        w->codes_plane_stride != 0 || w->scales_plane_stride != 0)
+      return TQ_ERR_INVALID_ARG;
+    if (w->scales == nullptr) return TQ_ERR_INVALID_ARG;
+    if (w->format == TQ_FMT_MX4 && w->lut != nullptr) return TQ_ERR_INVALID_ARG;
+    if (w->group != 0 && w->group != block) return TQ_ERR_UNSUPPORTED;
+    if (w->k_cols % 32 != 0) return TQ_ERR_SHAPE;
+    if (!aligned(w->codes, 16) || !aligned(w->scales, 16) ||
+        !aligned(w->lut, 4))
+      return TQ_ERR_ALIGNMENT;
+    v->group = block;
   } else {
     return TQ_ERR_INVALID_ARG;
   }
@@ -101,6 +115,11 @@ size_t tq_packed_bytes(int32_t format, int64_t n, int64_t k, int32_t group,
   if (format == TQ_FMT_B7) {
     if (k % 16 != 0) return 0;
     return (size_t)n * (size_t)(14 * (k / 16)) + 128u * 4u;
+  }
+  if (tq::is_f4(format)) {
+    if (k % 32 != 0) return 0;
+    return (size_t)n * (size_t)(k / 2 + k / tq::f4_block(format)) +
+           (format == TQ_FMT_NV4 ? 4u : 0u);
   }
   return 0;
 }
@@ -155,6 +174,29 @@ tq_status tq_unpack(const tq_weights *w, void *W_bf16_out, int32_t *dev_status,
                                      static_cast<cudaStream_t>(cuda_stream)));
 }
 
+tq_status tq_quantize_f4(const void *W_bf16, int64_t n, int64_t k, int64_t ldw,
+                         int32_t format, uint8_t *codes_out,
+                         uint8_t *scales_out, float *tensor_scale,
+                         int32_t scale_given, int32_t *dev_status,
+                         void *cuda_stream) {
+  if (!tq::is_f4(format) || n < 0 || k < 0) return TQ_ERR_INVALID_ARG;
+  if (n > 0 && k > 0 &&
+      (W_bf16 == nullptr || codes_out == nullptr || scales_out == nullptr))
+    return TQ_ERR_INVALID_ARG;
+  if ((format == TQ_FMT_NV4) != (tensor_scale != nullptr))
+    return TQ_ERR_INVALID_ARG;
+  if (format == TQ_FMT_MX4 && scale_given != 0) return TQ_ERR_INVALID_ARG;
+  if (k % 32 != 0 || ldw < k) return TQ_ERR_SHAPE;
+  if (!aligned(W_bf16, 16) || ldw % 8 != 0 || !aligned(codes_out, 16) ||
+      !aligned(scales_out, 16) || !aligned(tensor_scale, 4) ||
+      !aligned(dev_status, 4))
+    return TQ_ERR_ALIGNMENT;
+  return from_cuda(tq::launch_quantize_f4(
+      static_cast<const uint16_t *>(W_bf16), n, k, ldw, format, codes_out,
+      scales_out, tensor_scale, scale_given != 0, dev_status,
+      static_cast<cudaStream_t>(cuda_stream)));
+}
+
 tq_status tq_encode_b(const void *W_bf16, int64_t n, int64_t k,
                       const float ladder[5], float zeta,
                       int32_t rows_per_scale, uint8_t *codes_out,
@@ -198,6 +240,51 @@ tq_status tq_linear(const tq_weights *w, const void *x_bf16, int64_t batch,
   return from_cuda(tq::launch_linear(
       v, static_cast<const __nv_bfloat16 *>(x_bf16), batch, ldx, y, ldy,
       stream));
+}
+
+tq_status tq_linear_f4(const tq_weights *w, const tq_weights *x, void *y,
+                       int64_t ldy, int32_t y_type, void *cuda_stream) {
+  tq::WeightsView v, u;
+  tq_status st = check_weights(w, &v);
+  if (st != TQ_OK) return st;
+  if ((st = check_weights(x, &u)) != TQ_OK) return st;
+  if (!tq::is_f4(v.format) || u.format != v.format || y == nullptr)
+    return TQ_ERR_INVALID_ARG;
+  if (y_type != TQ_Y_F32 && y_type != TQ_Y_BF16) return TQ_ERR_INVALID_ARG;
+  if (u.k != v.k || ldy < v.n) return TQ_ERR_SHAPE;
+  if (!aligned(y, y_type == TQ_Y_F32 ? 4 : 2)) return TQ_ERR_ALIGNMENT;
+  if (v.n == 0 || u.n == 0) return TQ_OK;
+  cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+  if (v.k == 0) {  // empty sum: y = 0
+    const size_t es = y_type == TQ_Y_F32 ? 4 : 2;
+    return from_cuda(cudaMemset2DAsync(y, (size_t)ldy * es, 0,
+                                       (size_t)v.n * es, (size_t)u.n, stream));
+  }
+  return from_cuda(tq::launch_linear_f4(v, u, y, ldy, y_type, stream));
+}
+
+tq_status tq_linear_experts_f4(const tq_weights *w, int32_t n_experts,
+                               const int32_t *ids, int64_t n_tokens,
+                               const void *x_bf16, int64_t ldx, float *y,
+                               int64_t ldy, int32_t *dev_status,
+                               void *cuda_stream) {
+  tq::WeightsView v;
+  const tq_status st = check_weights(w, &v);
+  if (st != TQ_OK) return st;
+  if (!tq::is_f4(v.format) || n_tokens < 0 || n_experts < 1)
+    return TQ_ERR_INVALID_ARG;
+  if (v.n < 1 || v.k < 32) return TQ_ERR_SHAPE;
+  if (n_tokens > 65535 || n_experts > 65535) return TQ_ERR_UNSUPPORTED;
+  if (n_tokens == 0) return TQ_OK;
+  if (ids == nullptr || x_bf16 == nullptr || y == nullptr)
+    return TQ_ERR_INVALID_ARG;
+  if (ldx < v.k || ldy < v.n) return TQ_ERR_SHAPE;
+  if (!aligned(ids, 4) || !aligned(x_bf16, 16) || ldx % 8 != 0 ||
+      !aligned(y, 4) || !aligned(dev_status, 4))
+    return TQ_ERR_ALIGNMENT;
+  return from_cuda(tq::launch_linear_experts_f4(
+      v, n_experts, ids, n_tokens, static_cast<const __nv_bfloat16 *>(x_bf16),
+      ldx, y, ldy, dev_status, static_cast<cudaStream_t>(cuda_stream)));
 }
 
 tq_status tq_pack7(const uint8_t *codes, int64_t n, int64_t k,

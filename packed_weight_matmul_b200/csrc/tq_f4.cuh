@@ -1,0 +1,68 @@
+// 4-bit floats with a scale per block (TQ_FMT_MX4, TQ_FMT_NV4): device
+// helpers and launchers. E2M1 codes are decoded by the conversion
+// instructions of sm_100a (two codes per byte -> two fp16, exact).
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "tq_common.cuh"
+
+namespace tq {
+
+__host__ __device__ constexpr bool is_f4(int format) {
+  return format == TQ_FMT_MX4 || format == TQ_FMT_NV4;
+}
+__host__ __device__ constexpr int f4_block(int format) {
+  return format == TQ_FMT_MX4 ? 32 : 16;
+}
+
+// The 8 codes of a word as fp16 pairs: h[i] holds the codes of byte i, the
+// low four bits in the low half.
+__device__ __forceinline__ void f4x8_to_h2(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %4;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, b0;\n cvt.rn.f16x2.e2m1x2 %1, b1;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, b2;\n cvt.rn.f16x2.e2m1x2 %3, b3;\n}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+
+// E8M0 byte -> fp32: 2^(b - 127), 255 is NaN (b = 0 is the subnormal 2^-127).
+__device__ __forceinline__ float e8m0_to_f32(uint32_t b) {
+  return b == 255u ? __int_as_float(0x7FC00000)
+                   : __uint_as_float(b == 0u ? 0x00400000u : b << 23);
+}
+
+// E4M3 byte without its sign bit -> fp32 (0x7F is NaN).
+__device__ __forceinline__ float e4m3_to_f32(uint32_t b) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(b & 0x7Fu)));
+  return __half2float(__ushort_as_half((unsigned short)h));
+}
+
+template <int FMT>
+__device__ __forceinline__ float f4_scale(uint32_t b) {
+  return FMT == TQ_FMT_MX4 ? e8m0_to_f32(b) : e4m3_to_f32(b);
+}
+
+cudaError_t launch_quantize_f4(const uint16_t *W, int64_t n, int64_t k,
+                               int64_t ldw, int format, uint8_t *codes,
+                               uint8_t *scales, float *tensor_scale,
+                               bool given, int32_t *status,
+                               cudaStream_t stream);
+cudaError_t launch_unpack_f4(const WeightsView &w, uint16_t *out,
+                             int32_t *status, cudaStream_t stream);
+// y = x W^T, bf16 x (tq_linear with a 4-bit descriptor).
+cudaError_t linear_f4_bf16(const WeightsView &w, const __nv_bfloat16 *x,
+                           int64_t batch, int64_t ldx, float *y, int64_t ldy,
+                           cudaStream_t stream);
+cudaError_t launch_linear_experts_f4(const WeightsView &w, int n_experts,
+                                     const int32_t *ids, int64_t tokens,
+                                     const __nv_bfloat16 *x, int64_t ldx,
+                                     float *y, int64_t ldy, int32_t *status,
+                                     cudaStream_t stream);
+// y = x W^T, both in 4 bits.
+cudaError_t launch_linear_f4(const WeightsView &w, const WeightsView &x,
+                             void *y, int64_t ldy, int y_type,
+                             cudaStream_t stream);
+
+}  // namespace tq

@@ -10,6 +10,7 @@
 // This is the validation and cross-check path, not the matmul: it writes the
 // bf16 matrix the fused kernels never materialise.
 #include "tq_common.cuh"
+#include "tq_f4.cuh"
 
 namespace tq {
 namespace {
@@ -187,6 +188,7 @@ cudaError_t launch_a(const WeightsView &w, uint16_t *out, int32_t *status,
 
 cudaError_t launch_unpack(const WeightsView &w, uint16_t *out,
                           int32_t *status, cudaStream_t stream) {
+  if (is_f4(w.format)) return launch_unpack_f4(w, out, status, stream);
   if (w.format == TQ_FMT_A) {
     if (w.group == 64)
       return w.planes == 1 ? launch_a<64, 1>(w, out, status, stream)

@@ -19,7 +19,9 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)),
 TQ_OK, TQ_ERR_INVALID_ARG, TQ_ERR_SHAPE, TQ_ERR_ALIGNMENT = 0, 1, 2, 3
 TQ_ERR_UNSUPPORTED, TQ_ERR_BAD_CODE, TQ_ERR_NONFINITE = 4, 5, 6
 TQ_ERR_RANGE, TQ_ERR_TIMEOUT, TQ_ERR_CUDA = 7, 8, 9
-TQ_FMT_A, TQ_FMT_B, TQ_FMT_B7 = 1, 2, 3
+TQ_FMT_A, TQ_FMT_B, TQ_FMT_B7, TQ_FMT_MX4, TQ_FMT_NV4 = 1, 2, 3, 4, 5
+TQ_Y_F32, TQ_Y_BF16 = 0, 1
+F4_BLOCK = {TQ_FMT_MX4: 32, TQ_FMT_NV4: 16}
 
 # Every entry point declared in include/tq.h.
 ENTRY_POINTS = ("tq_packed_bytes", "tq_build_lut", "tq_quantize_pack",
@@ -27,7 +29,8 @@ ENTRY_POINTS = ("tq_packed_bytes", "tq_build_lut", "tq_quantize_pack",
                 "tq_encode_b", "tq_testing_linear_wait_fault",
                 "tq_testing_force_linear_path", "tq_testing_tc_self_check",
                 "tq_testing_tc_trace", "tq_linear_experts", "tq_pack7",
-                "tq_build_lut7", "tq_testing_tc_split")
+                "tq_build_lut7", "tq_testing_tc_split", "tq_quantize_f4",
+                "tq_linear_f4", "tq_linear_experts_f4")
 
 
 class TqError(RuntimeError):
@@ -93,6 +96,14 @@ def _load():
     L.tq_linear_experts.restype = C.c_int
     L.tq_linear_experts.argtypes = [C.POINTER(tq_experts), P, i64, P, i64, P,
                                     i64, P, P]
+    L.tq_quantize_f4.restype = C.c_int
+    L.tq_quantize_f4.argtypes = [P, i64, i64, i64, i32, P, P, P, i32, P, P]
+    L.tq_linear_f4.restype = C.c_int
+    L.tq_linear_f4.argtypes = [C.POINTER(tq_weights), C.POINTER(tq_weights),
+                               P, i64, i32, P]
+    L.tq_linear_experts_f4.restype = C.c_int
+    L.tq_linear_experts_f4.argtypes = [C.POINTER(tq_weights), i32, P, i64, P,
+                                       i64, P, i64, P, P]
     return L
 
 
@@ -306,6 +317,30 @@ def weights_b(codes, lut, rho=None, rows_per_scale=0, n=None, k=None,
     return Weights(d, (codes, lut, rho))
 
 
+def _weights_f4(fmt, codes, scales, lut, n, k) -> Weights:
+    if n is None:
+        n, k = codes.shape[0], codes.shape[1] * 2
+    d = tq_weights(format=fmt, group=F4_BLOCK[fmt], planes=1,
+                   rows_per_scale=0, n_rows=n, k_cols=k, codes=_ptr(codes),
+                   scales=_ptr(scales), lut=_ptr(lut), codes_plane_stride=0,
+                   scales_plane_stride=0, lut_rows=0)
+    return Weights(d, (codes, scales, lut))
+
+
+def weights_mx4(codes, scales, n=None, k=None) -> Weights:
+    """4-bit floats, blocks of 32: codes [n][k/2] (low four bits = lower k),
+    E8M0 scale bytes [n][k/32]. For tq_linear_experts_f4: the stacked experts,
+    n the rows of one."""
+    return _weights_f4(TQ_FMT_MX4, codes, scales, None, n, k)
+
+
+def weights_nv4(codes, scales, tensor_scale=None, n=None, k=None) -> Weights:
+    """4-bit floats, blocks of 16: codes [n][k/2], E4M3 scale bytes [n][k/16]
+    and the fp32 tensor scale (device, 1 value; one per expert for
+    tq_linear_experts_f4; None: 1)."""
+    return _weights_f4(TQ_FMT_NV4, codes, scales, tensor_scale, n, k)
+
+
 # ---- GPU entry points -----------------------------------------------------------
 
 def tq_quantize_pack(W, group, planes, codes_out, scales_out, dev_status=None,
@@ -359,4 +394,84 @@ def tq_linear(w: Weights, x, y, batch=None, ldx=None, ldy=None, stream=None,
                         _stream(stream))
     if check:
         _check(st, "tq_linear")
+    return st
+
+
+def _f4_tensor(t, dtypes, what):
+    """The 4-bit entry points check what the C ABI cannot see of a tensor:
+    that it lies on the current device, with the element type it is read as
+    and dense rows."""
+    if t.device.type != "cuda" or \
+            t.device.index != torch.cuda.current_device():
+        raise TqError(TQ_ERR_INVALID_ARG, f"{what}: not on the current device")
+    if t.dtype not in dtypes:
+        raise TqError(TQ_ERR_INVALID_ARG, f"{what}: {t.dtype}")
+    if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise TqError(TQ_ERR_INVALID_ARG, f"{what}: rows are not dense")
+
+
+def _rows(t):
+    """Distance of a matrix's rows (any value is right for a single row)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+_U8 = (torch.uint8, torch.int8, torch.float8_e8m0fnu, torch.float8_e4m3fn)
+
+
+def tq_quantize_f4(W, fmt, codes_out, scales_out, tensor_scale=None,
+                   scale_given=False, dev_status=None, stream=None,
+                   check=True):
+    """Quantize the rows of a bf16 matrix (row stride free) to 4-bit floats:
+    codes_out uint8 [n][k/2], scales_out bytes [n][k/32] (TQ_FMT_MX4) or
+    [n][k/16] (TQ_FMT_NV4). NV4: tensor_scale is read when scale_given, else
+    written."""
+    n, k = W.shape
+    _f4_tensor(W, (torch.bfloat16,), "tq_quantize_f4: W")
+    _f4_tensor(codes_out, (torch.uint8,), "tq_quantize_f4: codes_out")
+    _f4_tensor(scales_out, _U8, "tq_quantize_f4: scales_out")
+    if codes_out.numel() < n * (k // 2) or not codes_out.is_contiguous() or \
+            scales_out.numel() < n * (k // F4_BLOCK.get(fmt, 16)) or \
+            not scales_out.is_contiguous():
+        raise TqError(TQ_ERR_SHAPE, "tq_quantize_f4: outputs")
+    if tensor_scale is not None:
+        _f4_tensor(tensor_scale, (torch.float32,), "tq_quantize_f4: scale")
+    st = _lib.tq_quantize_f4(W.data_ptr(), n, k, _rows(W), fmt,
+                             codes_out.data_ptr(), scales_out.data_ptr(),
+                             _ptr(tensor_scale), int(bool(scale_given)),
+                             _ptr(dev_status), _stream(stream))
+    if check:
+        _check(st, "tq_quantize_f4")
+    return st
+
+
+def tq_linear_f4(w: Weights, x: Weights, y, stream=None, check=True):
+    """y = x W^T of two 4-bit matrices of one format; y fp32 or bf16
+    [batch][n], row stride free."""
+    _f4_tensor(y, (torch.float32, torch.bfloat16), "tq_linear_f4: y")
+    if y.dim() != 2 or y.shape[0] < x.n or y.shape[1] < w.n:
+        raise TqError(TQ_ERR_SHAPE, "tq_linear_f4: y")
+    st = _lib.tq_linear_f4(C.byref(w.desc), C.byref(x.desc), y.data_ptr(),
+                           _rows(y), TQ_Y_BF16 if y.dtype == torch.bfloat16
+                           else TQ_Y_F32, _stream(stream))
+    if check:
+        _check(st, "tq_linear_f4")
+    return st
+
+
+def tq_linear_experts_f4(w: Weights, n_experts, ids, x, y, status=None,
+                         stream=None, check=True):
+    """y[t] = x[t] W_e^T with e = ids[t] (int32, device); w holds the stacked
+    experts, w.n the rows of one."""
+    _f4_tensor(ids, (torch.int32,), "tq_linear_experts_f4: ids")
+    _f4_tensor(x, (torch.bfloat16,), "tq_linear_experts_f4: x")
+    _f4_tensor(y, (torch.float32,), "tq_linear_experts_f4: y")
+    t = ids.shape[0]
+    if x.shape[0] < t or y.shape[0] < t or x.shape[1] < w.k or \
+            y.shape[1] < w.n:
+        raise TqError(TQ_ERR_SHAPE, "tq_linear_experts_f4: x, y")
+    st = _lib.tq_linear_experts_f4(C.byref(w.desc), n_experts, ids.data_ptr(),
+                                   t, x.data_ptr(), _rows(x), y.data_ptr(),
+                                   _rows(y), _ptr(status), _stream(stream))
+    if check:
+        _check(st, "tq_linear_experts_f4")
     return st
