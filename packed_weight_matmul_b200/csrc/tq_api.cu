@@ -253,6 +253,9 @@ tq_status tq_linear_f4(const tq_weights *w, const tq_weights *x, void *y,
   if (y_type != TQ_Y_F32 && y_type != TQ_Y_BF16) return TQ_ERR_INVALID_ARG;
   if (u.k != v.k || ldy < v.n) return TQ_ERR_SHAPE;
   if (!aligned(y, y_type == TQ_Y_F32 ? 4 : 2)) return TQ_ERR_ALIGNMENT;
+  // row and column indices of the tensor copies are 32-bit
+  if (v.n > INT32_MAX / 2 || u.n > INT32_MAX / 2 || v.k > INT32_MAX / 2)
+    return TQ_ERR_UNSUPPORTED;
   if (v.n == 0 || u.n == 0) return TQ_OK;
   cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
   if (v.k == 0) {  // empty sum: y = 0

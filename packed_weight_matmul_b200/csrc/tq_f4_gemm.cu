@@ -1,0 +1,558 @@
+// Product of two 4-bit matrices of one format (tq_linear_f4) on the
+// block-scaled tensor cores of sm_100a:
+//
+//   y[b][n] = g_w g_x sum_k c_w[n][k] s_w[n][k/B] c_x[b][k] s_x[b][k/B]
+//
+// tcgen05.mma kind::mxf4 (MX4: E8M0 scale per 32) and kind::mxf4nvf4 (NV4:
+// E4M3 scale per 16) multiply the packed codes as they lie in memory: codes
+// go from global to shared memory by TMA and are never decoded. The block
+// scales of both operands have to sit in tensor memory, row r of a 128-row
+// operand at lane r % 32 (repeated in all four lane quarters) and column
+// r / 32, one 32-bit column word per row holding the scales of 128 (MX4) or
+// 64 (NV4) consecutive k.
+//
+// A tile is CG * 128 weight rows (M) times NT batch rows (N); CG = 2 pairs
+// the CTAs of a cluster on one tile (each holds its 128 weight rows and half
+// of the batch rows). Persistent, 16 warps per CTA:
+//   warp 0       TMA producer: per stage of 256 k the 128-byte swizzled boxes
+//                of the weight rows and of this CTA's batch rows
+//   warp 1       MMA issuer (of the pair's first CTA): 4 MMAs of K = 64
+//   warp 2       tensor-memory allocation
+//   warps 4-7    scales: rows are copied as they lie ([row][8 or 16 bytes]) to
+//                shared memory; every warp reads rows lane, lane + 32, ... and
+//                stores word w of row group i to column 4 w + i of its own
+//                lane quarter, which is the transposition the layout needs
+//   warps 8-15   epilogue: tensor memory -> registers -> y
+//
+// Every wait is bounded; one that gives up leaves NaN in the outputs of the
+// tiles that were not finished.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "tq_f4.cuh"
+#include "tq_sm100_async.cuh"
+#include "tq_sm100_mma.cuh"
+
+namespace tq {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kRowsM = 128;         // weight rows per CTA
+constexpr uint32_t kStageRow = 128; // code bytes of a row per stage (256 k)
+constexpr uint32_t kTmemColumns = 512;
+constexpr uint32_t kSmemLimit = 227u * 1024u;
+constexpr int kScaleWarps = 4, kDrainWarps = 8;
+
+template <int FMT, int NT, int CG>
+struct Plan {
+  static constexpr int kWords = FMT == TQ_FMT_MX4 ? 2 : 4;  // scale words/row
+  static constexpr uint32_t kScaleRow = kWords * 4;  // scale bytes per stage
+  static constexpr uint32_t kBCols = NT / 32 > 4 ? NT / 32 : 4;
+  static constexpr uint32_t kScaleCols = kWords * (4 + kBCols);
+  static constexpr uint32_t kA = kRowsM * kStageRow;
+  static constexpr uint32_t kB = (NT / CG) * kStageRow;
+  static constexpr uint32_t kScales = (kRowsM + NT) * kScaleRow;
+  static constexpr uint32_t kStage = kA + kB + kScales;
+  static constexpr int kFit = (int)((kSmemLimit - 3072u) / kStage);
+  static constexpr int kFitT = (int)((kTmemColumns - NT) / kScaleCols);
+  static constexpr int kStages0 = kFit < kFitT ? kFit : kFitT;
+  static constexpr int kStages = kStages0 < 8 ? kStages0 : 8;
+  static_assert(kStages >= 3, "ring too short");
+  // offsets from the 1024-byte aligned base
+  static constexpr uint32_t kOffB = kStages * kA;
+  static constexpr uint32_t kOffS = kOffB + kStages * kB;
+  static constexpr uint32_t kOffBar = kOffS + kStages * kScales;
+  static constexpr uint32_t kSmem = kOffBar + 512 + 1024;
+  static_assert(kSmem <= kSmemLimit, "shared memory");
+};
+
+struct Args {
+  const uint8_t *wscales, *xscales;
+  const float *wg, *xg;
+  void *y;
+  int64_t n, batch, ldy;
+  int k, tiles_m, tiles_n, y_bf16;
+};
+
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t a, uint32_t b,
+                                         uint32_t c, uint32_t d) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::
+                   "r"(taddr),
+               "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void alloc_columns(uint32_t dst, uint32_t cols) {
+  if constexpr (CG == 1) {
+    tmem_alloc(dst, cols);
+  } else {
+    asm volatile(
+        "tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+            dst),
+        "r"(cols)
+        : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::
+                     : "memory");
+  }
+}
+
+template <int CG>
+__device__ __forceinline__ void free_columns(uint32_t taddr, uint32_t cols) {
+  if constexpr (CG == 1)
+    tmem_dealloc(taddr, cols);
+  else
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(
+                     taddr),
+                 "r"(cols)
+                 : "memory");
+}
+
+// Arrive on `bar` (of both CTAs of a pair) when all MMAs issued so far by
+// this thread are complete.
+template <int CG>
+__device__ __forceinline__ void commit(uint32_t bar) {
+  if constexpr (CG == 1)
+    mma_commit(bar);
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster."
+        "multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+// D (+)= (A * scale A)(B * scale B)^T over 64 k.
+template <int FMT, int CG>
+__device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b,
+                                           uint32_t idesc, uint32_t sa,
+                                           uint32_t sb, uint32_t accumulate) {
+#define TQ_MMA(GROUP, KIND)                                                   \
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"                  \
+               " tcgen05.mma.cta_group::" GROUP ".kind::" KIND                \
+               " [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),               \
+               "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)  \
+               : "memory")
+  if constexpr (FMT == TQ_FMT_MX4 && CG == 1)
+    TQ_MMA("1", "mxf4.block_scale.scale_vec::2X");
+  else if constexpr (FMT == TQ_FMT_MX4)
+    TQ_MMA("2", "mxf4.block_scale.scale_vec::2X");
+  else if constexpr (CG == 1)
+    TQ_MMA("1", "mxf4nvf4.block_scale.scale_vec::4X");
+  else
+    TQ_MMA("2", "mxf4nvf4.block_scale.scale_vec::4X");
+#undef TQ_MMA
+}
+
+// Instruction descriptor of the 4-bit kinds: scale byte of B at bits 4-5 and
+// of A at 29-30 (first of the word's bytes that this MMA uses), E2M1 = 1 at
+// 7-9 and 10-12, N >> 3 at 17-22, E8M0 scales at 23, M >> 4 at 24-28.
+template <int FMT>
+__host__ __device__ constexpr uint32_t idesc_f4(int M, int N, uint32_t byte) {
+  return (byte << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) |
+         ((FMT == TQ_FMT_MX4 ? 1u : 0u) << 23) | ((uint32_t)(M >> 4) << 24) |
+         (byte << 29);
+}
+
+__device__ __forceinline__ void cp_async(uint32_t dst, const void *src,
+                                         int bytes) {
+  if (bytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst),
+                 "l"(src)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst),
+                 "l"(src)
+                 : "memory");
+}
+
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// One row's scale bytes of a stage into shared memory. Rows whose length is a
+// multiple of a stage's bytes start aligned and go by cp.async; others are
+// read byte by byte, and bytes past the row's end become 0 (their codes are
+// zero too).
+template <uint32_t BYTES>
+__device__ __forceinline__ void load_scales(uint32_t dst, const uint8_t *row,
+                                            int64_t row_bytes, int64_t off,
+                                            bool whole) {
+  if (whole) {
+    cp_async(dst, row + off, BYTES);
+    return;
+  }
+#pragma unroll
+  for (int w = 0; w < (int)BYTES / 4; ++w) {
+    uint32_t v = 0;
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+      if (off + 4 * w + b < row_bytes)
+        v |= (uint32_t)__ldg(row + off + 4 * w + b) << (8 * b);
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + 4 * w), "r"(v)
+                 : "memory");
+  }
+}
+
+template <int FMT, int NT, int CG>
+__global__ void __launch_bounds__(kThreads, 1)
+    product_f4_kernel(const __grid_constant__ CUtensorMap tmap_w,
+                      const __grid_constant__ CUtensorMap tmap_x,
+                      const Args args) {
+  using P = Plan<FMT, NT, CG>;
+  constexpr int S = P::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t bars = base + P::kOffBar;
+  const uint32_t full = bars, ready = bars + 8 * S, empty = bars + 16 * S;
+  const uint32_t dfull = bars + 24 * S, dempty = dfull + 8;
+  const uint32_t slot = dfull + 16, abort_addr = dfull + 20;
+  const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
+  const int group = blockIdx.x / CG, groups = gridDim.x / CG;
+  const int tiles = args.tiles_m * args.tiles_n;
+  const int steps = (args.k + 255) / 256;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full + 8 * s, 1);
+      mbar_init(ready + 8 * s, CG * kScaleWarps);
+      mbar_init(empty + 8 * s, 1);
+    }
+    mbar_init(dfull, 1);
+    mbar_init(dempty, CG * kDrainWarps);
+    st_volatile_s32(abort_addr, 0);
+    mbar_init_fence();
+  }
+  if (warp == 2) alloc_columns<CG>(slot, kTmemColumns);
+  tc_fence_before_sync();
+  __syncthreads();
+  if (CG == 2) {
+    asm volatile("barrier.cluster.arrive.aligned;\n"
+                 "barrier.cluster.wait.aligned;" ::: "memory");
+  }
+  tc_fence_after_sync();
+  const uint32_t tmem = (uint32_t)ld_volatile_s32(slot);
+  const uint32_t tmem_scales = tmem + NT;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t it = 0;
+      bool ok = true;
+      for (int t = group; t < tiles && ok; t += groups) {
+        const int m0 = (t / args.tiles_n) * (CG * kRowsM) + rank * kRowsM;
+        const int b0 = (t % args.tiles_n) * NT + rank * (NT / CG);
+        for (int i = 0; i < steps; ++i, ++it) {
+          const uint32_t s = it % S, ph = (it / S) & 1u;
+          ok = mbar_wait(empty + 8 * s, ph ^ 1u, abort_addr, kWaitLimitNs);
+          if (!ok) break;
+          mbar_arrive_expect_tx(full + 8 * s, P::kA + P::kB);
+          tma_load_2d(base + s * P::kA, &tmap_w, i * (int)kStageRow, m0,
+                      full + 8 * s);
+          tma_load_2d(base + P::kOffB + s * P::kB, &tmap_x,
+                      i * (int)kStageRow, b0, full + 8 * s);
+        }
+      }
+      // every copy issued has landed, and every MMA that read one is done
+      for (uint32_t j = it > (uint32_t)S ? it - S : 0; j < it; ++j) {
+        const uint32_t s = j % S, ph = (j / S) & 1u;
+        mbar_wait(full + 8 * s, ph);
+        mbar_wait(empty + 8 * s, ph, abort_addr, kWaitLimitNs);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      uint32_t it = 0, done = 0;
+      bool ok = true;
+      for (int t = group; t < tiles && ok; t += groups, ++done) {
+        if (done > 0)
+          ok = mbar_wait_cluster(dempty, (done - 1) & 1u, abort_addr,
+                                 kWaitLimitNs);
+        if (!ok) break;
+        for (int i = 0; i < steps; ++i, ++it) {
+          const uint32_t s = it % S, ph = (it / S) & 1u;
+          ok = mbar_wait_cluster(ready + 8 * s, ph, abort_addr, kWaitLimitNs);
+          if (!ok) break;
+          tc_fence_after_sync();
+          const uint64_t a = smem_desc_kmajor_sw128(base + s * P::kA);
+          const uint64_t b =
+              smem_desc_kmajor_sw128(base + P::kOffB + s * P::kB);
+          const uint32_t sa = tmem_scales + s * P::kScaleCols;
+          const uint32_t sb = sa + P::kWords * 4;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int w = FMT == TQ_FMT_MX4 ? j / 2 : j;
+            const uint32_t byte = FMT == TQ_FMT_MX4 ? (j & 1) * 2u : 0u;
+            mma_scaled<FMT, CG>(tmem, a + 2 * j, b + 2 * j,
+                                idesc_f4<FMT>(CG * kRowsM, NT, byte),
+                                sa + 4 * w, sb + P::kBCols * w,
+                                (i | j) != 0 ? 1u : 0u);
+          }
+          commit<CG>(empty + 8 * s);
+        }
+        if (ok) commit<CG>(dfull);
+      }
+      // every MMA issued is done before the CTA goes on to free its memory
+      for (uint32_t j = it > (uint32_t)S ? it - S : 0; j < it; ++j)
+        mbar_wait(empty + 8 * (j % S), (j / S) & 1u);
+    }
+  } else if (warp >= 4 && warp < 8) {
+    const int tid = threadIdx.x - 128;
+    const uint32_t quarter = (uint32_t)(warp & 3) << 21;  // lane 32 q, bits 16+
+    const int64_t row_bytes = args.k / (FMT == TQ_FMT_MX4 ? 32 : 16);
+    const bool whole = args.k % 256 == 0;
+    // the stage that is loaded next, ahead of the one in use
+    int lt = group, li = 0;
+    uint32_t lit = 0;
+    auto load = [&]() {
+      if (lt < tiles) {
+        const int64_t m0 =
+            (int64_t)(lt / args.tiles_n) * (CG * kRowsM) + rank * kRowsM;
+        const int64_t b0 = (int64_t)(lt % args.tiles_n) * NT;
+        const uint32_t dst = base + P::kOffS + (lit % S) * P::kScales;
+        const int64_t off = (int64_t)li * P::kScaleRow;
+        const int64_t m = m0 + tid < args.n ? m0 + tid : args.n - 1;
+        load_scales<P::kScaleRow>(dst + tid * P::kScaleRow,
+                                  args.wscales + m * row_bytes, row_bytes, off,
+                                  whole);
+#pragma unroll
+        for (int r = 0; r < (NT + 127) / 128; ++r) {
+          const int j = tid + 128 * r;
+          if (NT >= 128 || j < NT) {
+            const int64_t b = b0 + j < args.batch ? b0 + j : args.batch - 1;
+            load_scales<P::kScaleRow>(dst + (kRowsM + j) * P::kScaleRow,
+                                      args.xscales + b * row_bytes, row_bytes,
+                                      off, whole);
+          }
+        }
+        ++lit;
+        if (++li == steps) {
+          li = 0;
+          lt += groups;
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll 1
+    for (int p = 0; p < S - 1; ++p) load();
+    uint32_t it = 0;
+    bool ok = true;
+    for (int t = group; t < tiles; t += groups) {
+      for (int i = 0; i < steps; ++i, ++it) {
+        const uint32_t s = it % S, ph = (it / S) & 1u;
+        asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+        bar_sync(1, 128);  // stage `it` is here; `it - 1` has been read
+        load();
+        const uint32_t src = base + P::kOffS + s * P::kScales;
+        uint32_t a[4][P::kWords], b[P::kBCols][P::kWords];
+#pragma unroll
+        for (int r = 0; r < 4 + NT / 32 + (NT < 32); ++r) {
+          const uint32_t at = src + (32 * r + lane) * P::kScaleRow;
+          uint32_t *v = r < 4 ? a[r] : b[r - 4];
+          if constexpr (P::kWords == 2)
+            asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];"
+                         : "=r"(v[0]), "=r"(v[1])
+                         : "r"(at));
+          else
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(v[0]), "=r"(v[1]), "=r"(v[P::kWords - 2]),
+                           "=r"(v[P::kWords - 1])
+                         : "r"(at));
+          if (FMT == TQ_FMT_NV4) {  // scales are read without a sign
+#pragma unroll
+            for (int w = 0; w < P::kWords; ++w) v[w] &= 0x7F7F7F7Fu;
+          }
+        }
+#pragma unroll
+        for (int r = NT / 32 + (NT < 32); r < (int)P::kBCols; ++r)
+#pragma unroll
+          for (int w = 0; w < P::kWords; ++w) b[r][w] = 0;
+        // the MMAs that read this slot's scales before are done; after a wait
+        // that gave up, the warps only keep meeting at the barrier above
+        if (ok)
+          ok = mbar_wait(empty + 8 * s, ph ^ 1u, abort_addr, kWaitLimitNs);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (ok) {
+          tc_fence_after_sync();
+          const uint32_t sa = tmem_scales + s * P::kScaleCols + quarter;
+          const uint32_t sb = sa + P::kWords * 4;
+#pragma unroll
+          for (int w = 0; w < P::kWords; ++w) {
+            tmem_st4(sa + 4 * w, a[0][w], a[1][w], a[2][w], a[3][w]);
+#pragma unroll
+            for (int r = 0; r < (int)P::kBCols; r += 4)
+              tmem_st4(sb + P::kBCols * w + r, b[r][w], b[r + 1][w],
+                       b[r + 2][w], b[r + 3][w]);
+          }
+          tmem_st_wait();
+          tc_fence_before_sync();
+          // this CTA's codes are here as well
+          ok = mbar_wait(full + 8 * s, ph, abort_addr, kWaitLimitNs);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (ok && lane == 0) mbar_arrive_cluster(ready + 8 * s, 0);
+        }
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp >= 8) {
+    const int q = warp & 3, half = (warp - 8) >> 2;  // lane quarter, columns
+    constexpr int kCols = NT / 2;
+    constexpr int kChunk = kCols < 16 ? 8 : 16;
+    const float g = (args.wg != nullptr ? *args.wg : 1.0f) *
+                    (args.xg != nullptr ? *args.xg : 1.0f);
+    uint32_t done = 0;
+    bool ok = true;
+    for (int t = group; t < tiles; t += groups, ++done) {
+      if (ok) {
+        ok = mbar_wait(dfull, done & 1u, abort_addr, kWaitLimitNs);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+      }
+      tc_fence_after_sync();
+      const int64_t row = (int64_t)(t / args.tiles_n) * (CG * kRowsM) +
+                          rank * kRowsM + 32 * q + lane;
+      const int64_t b0 = (int64_t)(t % args.tiles_n) * NT + half * kCols;
+      const uint32_t src = tmem + half * kCols + ((uint32_t)q << 21);
+#pragma unroll 1
+      for (int c = 0; c < kCols; c += kChunk) {
+        uint32_t v[16];
+        if (ok) {
+          tmem_ld16(src + c, v);  // the last 8 of a chunk of 8 are not used
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] = 0x7FC00000u;
+        }
+        if (row < args.n) {
+#pragma unroll
+          for (int j = 0; j < kChunk; ++j) {
+            const int64_t b = b0 + c + j;
+            const float f = __uint_as_float(v[j]) * g;
+            if (b < args.batch) {
+              if (args.y_bf16)
+                static_cast<__nv_bfloat16 *>(args.y)[b * args.ldy + row] =
+                    __float2bfloat16_rn(f);
+              else
+                static_cast<float *>(args.y)[b * args.ldy + row] = f;
+            }
+          }
+        }
+        __syncwarp();
+      }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (ok && lane == 0) mbar_arrive_cluster(dempty, 0);
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before_sync();
+  __syncthreads();
+  if (CG == 2) {
+    asm volatile("barrier.cluster.arrive.aligned;\n"
+                 "barrier.cluster.wait.aligned;" ::: "memory");
+  }
+  if (warp == 2) {
+    tc_fence_after_sync();
+    free_columns<CG>(tmem, kTmemColumns);
+  }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault,
+                                &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+// Packed codes [rows][k/2]; boxes of 128 bytes (256 k) x `box` rows, 128-byte
+// swizzle. Rows and columns past the matrix read as zero codes.
+cudaError_t code_map(CUtensorMap *map, const WeightsView &w, int box_rows) {
+  auto encode = encode_fn();
+  if (encode == nullptr) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {(cuuint64_t)(w.k / 2), (cuuint64_t)w.n};
+  const cuuint64_t strides[1] = {(cuuint64_t)(w.k / 2)};
+  const cuuint32_t box[2] = {kStageRow, (cuuint32_t)box_rows};
+  const cuuint32_t estr[2] = {1u, 1u};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+                const_cast<uint8_t *>(w.codes), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
+template <int FMT, int NT, int CG>
+cudaError_t launch(const WeightsView &w, const WeightsView &x, void *y,
+                   int64_t ldy, int y_type, cudaStream_t stream) {
+  using P = Plan<FMT, NT, CG>;
+  int dev = 0, sms = 148;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  CUtensorMap mw, mx;
+  if ((e = code_map(&mw, w, kRowsM)) != cudaSuccess) return e;
+  if ((e = code_map(&mx, x, NT / CG)) != cudaSuccess) return e;
+  Args a = {};
+  a.wscales = reinterpret_cast<const uint8_t *>(w.scales);
+  a.xscales = reinterpret_cast<const uint8_t *>(x.scales);
+  a.wg = w.lut;
+  a.xg = x.lut;
+  a.y = y;
+  a.n = w.n;
+  a.batch = x.n;
+  a.ldy = ldy;
+  a.k = (int)w.k;
+  a.tiles_m = (int)((w.n + CG * kRowsM - 1) / (CG * kRowsM));
+  a.tiles_n = (int)((x.n + NT - 1) / NT);
+  a.y_bf16 = y_type == TQ_Y_BF16;
+  const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
+  const int groups = (int)(tiles < sms / CG ? tiles : sms / CG);
+  auto kern = product_f4_kernel<FMT, NT, CG>;
+  if ((e = ensure_smem_limit<product_f4_kernel<FMT, NT, CG>>(
+           (int)P::kSmem)) != cudaSuccess)
+    return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(groups * CG));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = P::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CG;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, mw, mx, a);
+}
+
+template <int FMT>
+cudaError_t dispatch(const WeightsView &w, const WeightsView &x, void *y,
+                     int64_t ldy, int y_type, cudaStream_t stream) {
+  if (x.n <= 32) return launch<FMT, 32, 1>(w, x, y, ldy, y_type, stream);
+  if (x.n <= 64) return launch<FMT, 64, 1>(w, x, y, ldy, y_type, stream);
+  if (x.n <= 128) return launch<FMT, 128, 1>(w, x, y, ldy, y_type, stream);
+  return launch<FMT, 256, 1>(w, x, y, ldy, y_type, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_linear_f4(const WeightsView &w, const WeightsView &x,
+                             void *y, int64_t ldy, int y_type,
+                             cudaStream_t stream) {
+  return w.format == TQ_FMT_MX4
+             ? dispatch<TQ_FMT_MX4>(w, x, y, ldy, y_type, stream)
+             : dispatch<TQ_FMT_NV4>(w, x, y, ldy, y_type, stream);
+}
+
+}  // namespace tq

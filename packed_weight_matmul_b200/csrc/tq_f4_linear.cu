@@ -82,43 +82,6 @@ __global__ void __launch_bounds__(kWarps * 32)
   }
 }
 
-template <int FMT>
-__global__ void __launch_bounds__(kWarps * 32)
-    product_kernel(const uint8_t *__restrict__ codes,
-                   const uint8_t *__restrict__ scales, const float *ts,
-                   int64_t n, int64_t k, const uint8_t *__restrict__ xcodes,
-                   const uint8_t *__restrict__ xscales, const float *xts,
-                   int64_t batch, void *y, int64_t ldy, int y_type) {
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (row >= n) return;
-  const float g =
-      (ts != nullptr ? *ts : 1.0f) * (xts != nullptr ? *xts : 1.0f);
-  for (int64_t b0 = blockIdx.y * kBatch; b0 < batch;
-       b0 += (int64_t)gridDim.y * kBatch) {
-    const int nb = (int)(batch - b0 < kBatch ? batch - b0 : kBatch);
-    float acc[kBatch] = {};
-    for (int64_t u = lane; u < k / 8; u += 32) {
-      float w[8], v[8];
-      weights8<FMT>(codes, scales, k, row, u, w);
-      for (int b = 0; b < nb; ++b) {
-        weights8<FMT>(xcodes, xscales, k, b0 + b, u, v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc[b] = fmaf(w[i], v[i], acc[b]);
-      }
-    }
-    for (int b = 0; b < nb; ++b) {
-      const float v = warp_sum(acc[b]) * g;
-      if (lane != 0) continue;
-      if (y_type == TQ_Y_BF16)
-        static_cast<__nv_bfloat16 *>(y)[(b0 + b) * ldy + row] =
-            __float2bfloat16_rn(v);
-      else
-        static_cast<float *>(y)[(b0 + b) * ldy + row] = v;
-    }
-  }
-}
-
 dim3 grid_of(int64_t n, int64_t batch, int64_t per) {
   const int64_t gy = (batch + per - 1) / per;
   return dim3((unsigned)((n + kWarps - 1) / kWarps),
@@ -148,18 +111,6 @@ cudaError_t launch_linear_experts_f4(const WeightsView &w, int n_experts,
   kern<<<grid_of(w.n, tokens, 1), kWarps * 32, 0, stream>>>(
       w.codes, reinterpret_cast<const uint8_t *>(w.scales), w.lut, w.n, w.k,
       ids, n_experts, x, tokens, ldx, y, ldy, status);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_linear_f4(const WeightsView &w, const WeightsView &x,
-                             void *y, int64_t ldy, int y_type,
-                             cudaStream_t stream) {
-  auto kern = w.format == TQ_FMT_MX4 ? product_kernel<TQ_FMT_MX4>
-                                     : product_kernel<TQ_FMT_NV4>;
-  kern<<<grid_of(w.n, x.n, kBatch), kWarps * 32, 0, stream>>>(
-      w.codes, reinterpret_cast<const uint8_t *>(w.scales), w.lut, w.n, w.k,
-      x.codes, reinterpret_cast<const uint8_t *>(x.scales), x.lut, x.n, y, ldy,
-      y_type);
   return cudaGetLastError();
 }
 

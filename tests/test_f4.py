@@ -157,6 +157,9 @@ def test_product_refusals(tq):
     assert call(ldy=3) == tq.TQ_ERR_SHAPE
     assert call(y=0x50002) == tq.TQ_ERR_ALIGNMENT
     assert call(y=0x50001, yt=1) == tq.TQ_ERR_ALIGNMENT
+    big = desc(tq, n_rows=1 << 30)
+    assert call(w=big, ldy=1 << 30) == tq.TQ_ERR_UNSUPPORTED
+    assert call(x=big) == tq.TQ_ERR_UNSUPPORTED
     a = tq.tq_weights(format=tq.TQ_FMT_A, group=64, planes=1, rows_per_scale=0,
                       n_rows=4, k_cols=128, codes=0x10000, scales=0x20000)
     assert call(w=a) == tq.TQ_ERR_INVALID_ARG
