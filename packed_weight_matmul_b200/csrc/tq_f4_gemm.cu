@@ -13,16 +13,21 @@
 //
 // A tile is CG * 128 weight rows (M) times NT batch rows (N); CG = 2 pairs
 // the CTAs of a cluster on one tile (each holds its 128 weight rows and half
-// of the batch rows). Persistent, 16 warps per CTA:
+// of the batch rows). Persistent, 18 warps per CTA:
 //   warp 0       TMA producer: per stage of 256 k the 128-byte swizzled boxes
-//                of the weight rows and of this CTA's batch rows
-//   warp 1       MMA issuer (of the pair's first CTA): 4 MMAs of K = 64
-//   warp 2       tensor-memory allocation
-//   warps 4-7    scales: rows are copied as they lie ([row][8 or 16 bytes]) to
-//                shared memory; every warp reads rows lane, lane + 32, ... and
-//                stores word w of row group i to column 4 w + i of its own
-//                lane quarter, which is the transposition the layout needs
-//   warps 8-15   epilogue: tensor memory -> registers -> y
+//                of the weight rows and of this CTA's batch rows; it also
+//                allocates the tensor memory
+//   warp 1       MMA issuer (first CTA of a pair): 4 MMAs of K = 64 per stage;
+//                in the second CTA it passes "stage ready" on to the first
+//   warps 2-9    scales, two groups of four warps that take turns. A group
+//                reads 32 bytes of scales of every row (one sector; 4 stages of
+//                MX4, 2 of NV4) into registers one turn ahead, lays them down
+//                row by row in shared memory, and then per stage every warp
+//                reads rows lane, lane + 32, ... and stores word w of row group
+//                i to column 4 w + i of its own lane quarter, which is the
+//                transposition the layout needs
+//   warps 10-17  epilogue: tensor memory -> registers -> y
+// A stage's barrier counts the four scale warps and the copies' bytes.
 //
 // Every wait is bounded; one that gives up leaves NaN in the outputs of the
 // tiles that were not finished.
@@ -38,12 +43,12 @@
 namespace tq {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 576;
 constexpr int kRowsM = 128;         // weight rows per CTA
 constexpr uint32_t kStageRow = 128; // code bytes of a row per stage (256 k)
 constexpr uint32_t kTmemColumns = 512;
 constexpr uint32_t kSmemLimit = 227u * 1024u;
-constexpr int kScaleWarps = 4, kDrainWarps = 8;
+constexpr int kScaleWarps = 4, kScaleGroups = 2, kDrainWarps = 8;
 
 template <int FMT, int NT, int CG>
 struct Plan {
@@ -53,17 +58,30 @@ struct Plan {
   static constexpr uint32_t kScaleCols = kWords * (4 + kBCols);
   static constexpr uint32_t kA = kRowsM * kStageRow;
   static constexpr uint32_t kB = (NT / CG) * kStageRow;
-  static constexpr uint32_t kScales = (kRowsM + NT) * kScaleRow;
-  static constexpr uint32_t kStage = kA + kB + kScales;
-  static constexpr int kFit = (int)((kSmemLimit - 3072u) / kStage);
+  static constexpr uint32_t kStage = kA + kB;
+  // scale bytes of a row that a group reads at once: a 32-byte sector where
+  // the ring is long enough (see the assertion below)
+  static constexpr uint32_t kUnit =
+      FMT == TQ_FMT_NV4 || 5 * kStage + 2 * (kRowsM + NT) * 32u + 3072u <=
+                               kSmemLimit
+          ? 32u
+          : 16u;
+  static constexpr int kUnitStages = (int)(kUnit / kScaleRow);
+  static constexpr uint32_t kScales = (kRowsM + NT) * kUnit;  // of one group
+  static constexpr int kFit =
+      (int)((kSmemLimit - 3072u - kScaleGroups * kScales) / kStage);
   static constexpr int kFitT = (int)((kTmemColumns - NT) / kScaleCols);
   static constexpr int kStages0 = kFit < kFitT ? kFit : kFitT;
   static constexpr int kStages = kStages0 < 8 ? kStages0 : 8;
-  static_assert(kStages >= 3, "ring too short");
+  // A wait by parity is right only one phase ahead. Between two units of a
+  // group lie up to kUnitStages stages of the other one, so the MMAs of stage
+  // it - 2 kStages are known to be done when a group waits for those of
+  // it - kStages only with kStages > kUnitStages.
+  static_assert(kStages > kUnitStages, "a group could run two phases ahead");
   // offsets from the 1024-byte aligned base
   static constexpr uint32_t kOffB = kStages * kA;
   static constexpr uint32_t kOffS = kOffB + kStages * kB;
-  static constexpr uint32_t kOffBar = kOffS + kStages * kScales;
+  static constexpr uint32_t kOffBar = kOffS + kScaleGroups * kScales;
   static constexpr uint32_t kSmem = kOffBar + 512 + 1024;
   static_assert(kSmem <= kSmemLimit, "shared memory");
 };
@@ -156,44 +174,43 @@ __host__ __device__ constexpr uint32_t idesc_f4(int M, int N, uint32_t byte) {
          (byte << 29);
 }
 
-__device__ __forceinline__ void cp_async(uint32_t dst, const void *src,
-                                         int bytes) {
-  if (bytes == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst),
-                 "l"(src)
-                 : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst),
-                 "l"(src)
-                 : "memory");
-}
-
 __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// One row's scale bytes of a stage into shared memory. Rows whose length is a
-// multiple of a stage's bytes start aligned and go by cp.async; others are
-// read byte by byte, and bytes past the row's end become 0 (their codes are
-// zero too).
-template <uint32_t BYTES>
-__device__ __forceinline__ void load_scales(uint32_t dst, const uint8_t *row,
-                                            int64_t row_bytes, int64_t off,
-                                            bool whole) {
+// 8 scale bytes of a row at `off`. Rows whose length is a multiple of 8 bytes
+// (k a multiple of 256) are read in one load, others byte by byte; bytes past
+// the row's end become 0 (their codes are zero too).
+template <int FMT>
+__device__ __forceinline__ uint2 load_scales8(const uint8_t *row, int row_bytes,
+                                              int off, bool whole) {
+  uint2 v = make_uint2(0u, 0u);
   if (whole) {
-    cp_async(dst, row + off, BYTES);
-    return;
-  }
+    if (off < row_bytes) v = __ldg(reinterpret_cast<const uint2 *>(row + off));
+  } else {
 #pragma unroll
-  for (int w = 0; w < (int)BYTES / 4; ++w) {
-    uint32_t v = 0;
-#pragma unroll
-    for (int b = 0; b < 4; ++b)
-      if (off + 4 * w + b < row_bytes)
-        v |= (uint32_t)__ldg(row + off + 4 * w + b) << (8 * b);
-    asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + 4 * w), "r"(v)
-                 : "memory");
+    for (int b = 0; b < 4; ++b) {
+      if (off + b < row_bytes) v.x |= (uint32_t)__ldg(row + off + b) << (8 * b);
+      if (off + 4 + b < row_bytes)
+        v.y |= (uint32_t)__ldg(row + off + 4 + b) << (8 * b);
+    }
   }
+  if (FMT == TQ_FMT_NV4) {  // E4M3 scales are read without their sign
+    v.x &= 0x7F7F7F7Fu;
+    v.y &= 0x7F7F7F7Fu;
+  }
+  return v;
+}
+
+// Where byte 8 c of row r's unit lies in a group's scale buffer: rows UNIT
+// bytes apart, the 8-byte (MX4) or 16-byte (NV4) pieces of a row swapped so
+// that the reads of one piece by 32 consecutive rows hit different banks.
+template <int FMT, uint32_t UNIT>
+__device__ __forceinline__ uint32_t scale_at(uint32_t r, uint32_t c) {
+  const uint32_t x = FMT == TQ_FMT_NV4 ? ((r >> 2) & 1u) << 1
+                     : UNIT == 32u     ? (r >> 2) & 3u
+                                       : (r >> 3) & 1u;
+  return r * UNIT + 8u * (c ^ x);
 }
 
 template <int FMT, int NT, int CG>
@@ -207,7 +224,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t bars = base + P::kOffBar;
-  const uint32_t full = bars, ready = bars + 8 * S, empty = bars + 16 * S;
+  // ready: a stage's codes and scales are here; peer: those of the pair's
+  // second CTA; empty: its MMAs are done
+  const uint32_t ready = bars, peer = bars + 8 * S, empty = bars + 16 * S;
   const uint32_t dfull = bars + 24 * S, dempty = dfull + 8;
   const uint32_t slot = dfull + 16, abort_addr = dfull + 20;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
@@ -217,8 +236,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(full + 8 * s, 1);
-      mbar_init(ready + 8 * s, CG * kScaleWarps);
+      mbar_init(ready + 8 * s, kScaleWarps + 1);
+      mbar_init(peer + 8 * s, 1);
       mbar_init(empty + 8 * s, 1);
     }
     mbar_init(dfull, 1);
@@ -226,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     st_volatile_s32(abort_addr, 0);
     mbar_init_fence();
   }
-  if (warp == 2) alloc_columns<CG>(slot, kTmemColumns);
+  if (warp == 0) alloc_columns<CG>(slot, kTmemColumns);
   tc_fence_before_sync();
   __syncthreads();
   if (CG == 2) {
@@ -248,21 +267,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t s = it % S, ph = (it / S) & 1u;
           ok = mbar_wait(empty + 8 * s, ph ^ 1u, abort_addr, kWaitLimitNs);
           if (!ok) break;
-          mbar_arrive_expect_tx(full + 8 * s, P::kA + P::kB);
+          mbar_arrive_expect_tx(ready + 8 * s, P::kA + P::kB);
           tma_load_2d(base + s * P::kA, &tmap_w, i * (int)kStageRow, m0,
-                      full + 8 * s);
+                      ready + 8 * s);
           tma_load_2d(base + P::kOffB + s * P::kB, &tmap_x,
-                      i * (int)kStageRow, b0, full + 8 * s);
+                      i * (int)kStageRow, b0, ready + 8 * s);
         }
       }
       // every copy issued has landed, and every MMA that read one is done
-      for (uint32_t j = it > (uint32_t)S ? it - S : 0; j < it; ++j) {
-        const uint32_t s = j % S, ph = (j / S) & 1u;
-        mbar_wait(full + 8 * s, ph);
-        mbar_wait(empty + 8 * s, ph, abort_addr, kWaitLimitNs);
-      }
+      for (uint32_t j = it > (uint32_t)S ? it - S : 0; j < it; ++j)
+        mbar_wait(empty + 8 * (j % S), (j / S) & 1u);
     }
   } else if (warp == 1) {
+    if (lane == 0 && rank == 1) {
+      uint32_t it = 0;
+      bool ok = true;
+      for (int t = group; t < tiles && ok; t += groups) {
+        for (int i = 0; i < steps && ok; ++i, ++it) {
+          ok = mbar_wait(ready + 8 * (it % S), (it / S) & 1u, abort_addr,
+                         kWaitLimitNs);
+          if (ok) mbar_arrive_cluster(peer + 8 * (it % S), 0);
+        }
+      }
+    }
     if (lane == 0 && rank == 0) {
       uint32_t it = 0, done = 0;
       bool ok = true;
@@ -273,7 +300,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         for (int i = 0; i < steps; ++i, ++it) {
           const uint32_t s = it % S, ph = (it / S) & 1u;
-          ok = mbar_wait_cluster(ready + 8 * s, ph, abort_addr, kWaitLimitNs);
+          ok = mbar_wait(ready + 8 * s, ph, abort_addr, kWaitLimitNs);
+          if (CG == 2)
+            ok = ok && mbar_wait_cluster(peer + 8 * s, ph, abort_addr,
+                                         kWaitLimitNs);
           if (!ok) break;
           tc_fence_after_sync();
           const uint64_t a = smem_desc_kmajor_sw128(base + s * P::kA);
@@ -298,151 +328,213 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint32_t j = it > (uint32_t)S ? it - S : 0; j < it; ++j)
         mbar_wait(empty + 8 * (j % S), (j / S) & 1u);
     }
-  } else if (warp >= 4 && warp < 8) {
-    const int tid = threadIdx.x - 128;
+  } else if (warp < 2 + kScaleWarps * kScaleGroups) {
+    const int turn = (warp - 2) / kScaleWarps;  // this warp's group
+    const int tid = (threadIdx.x - 64) & 127;
     const uint32_t quarter = (uint32_t)(warp & 3) << 21;  // lane 32 q, bits 16+
-    const int64_t row_bytes = args.k / (FMT == TQ_FMT_MX4 ? 32 : 16);
+    const int row_bytes = args.k / (FMT == TQ_FMT_MX4 ? 32 : 16);
     const bool whole = args.k % 256 == 0;
-    // the stage that is loaded next, ahead of the one in use
-    int lt = group, li = 0;
-    uint32_t lit = 0;
-    auto load = [&]() {
-      if (lt < tiles) {
-        const int64_t m0 =
-            (int64_t)(lt / args.tiles_n) * (CG * kRowsM) + rank * kRowsM;
-        const int64_t b0 = (int64_t)(lt % args.tiles_n) * NT;
-        const uint32_t dst = base + P::kOffS + (lit % S) * P::kScales;
-        const int64_t off = (int64_t)li * P::kScaleRow;
-        const int64_t m = m0 + tid < args.n ? m0 + tid : args.n - 1;
-        load_scales<P::kScaleRow>(dst + tid * P::kScaleRow,
-                                  args.wscales + m * row_bytes, row_bytes, off,
-                                  whole);
+    const uint32_t buf = base + P::kOffS + turn * P::kScales;
+    const int units = (steps + P::kUnitStages - 1) / P::kUnitStages;
+    // a row's unit is read by kUnit / 8 neighbouring threads
+    constexpr int kPieces = (int)P::kUnit / 8, kPass = 128 / kPieces;
+    constexpr int kRowsPer = (kRowsM + NT + kPass - 1) / kPass;
+    const int my_row = tid / kPieces, my_piece = tid % kPieces;
+    uint2 v[kRowsPer];
+    // unit `lu` of tile `lt`, into registers
+    auto load = [&](int lt, int lu) {
+      const int64_t m0 =
+          (int64_t)(lt / args.tiles_n) * (CG * kRowsM) + rank * kRowsM;
+      const int64_t b0 = (int64_t)(lt % args.tiles_n) * NT;
+      const int off = lu * (int)P::kUnit + 8 * my_piece;
 #pragma unroll
-        for (int r = 0; r < (NT + 127) / 128; ++r) {
-          const int j = tid + 128 * r;
-          if (NT >= 128 || j < NT) {
-            const int64_t b = b0 + j < args.batch ? b0 + j : args.batch - 1;
-            load_scales<P::kScaleRow>(dst + (kRowsM + j) * P::kScaleRow,
-                                      args.xscales + b * row_bytes, row_bytes,
-                                      off, whole);
-          }
-        }
-        ++lit;
-        if (++li == steps) {
-          li = 0;
-          lt += groups;
-        }
+      for (int j = 0; j < kRowsPer; ++j) {
+        const bool of_w = kPass * (j + 1) <= kRowsM;
+        const int64_t r = my_row + kPass * j;
+        int64_t at = of_w ? m0 + r : b0 + r - kRowsM;
+        const int64_t last = (of_w ? args.n : args.batch) - 1;
+        at = at < last ? at : last;
+        v[j] = load_scales8<FMT>(
+            (of_w ? args.wscales : args.xscales) + at * row_bytes, row_bytes,
+            off, whole);
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
     };
-#pragma unroll 1
-    for (int p = 0; p < S - 1; ++p) load();
-    uint32_t it = 0;
+    // (tile, unit) of this group's next turn: every second unit in order
+    int lt = group, lu = turn;
+    auto settle = [&]() {
+      while (lu >= units) {
+        lu -= units;
+        lt += groups;
+      }
+    };
+    settle();
+    if (lt < tiles) load(lt, lu);
     bool ok = true;
-    for (int t = group; t < tiles; t += groups) {
-      for (int i = 0; i < steps; ++i, ++it) {
-        const uint32_t s = it % S, ph = (it / S) & 1u;
-        asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
-        bar_sync(1, 128);  // stage `it` is here; `it - 1` has been read
-        load();
-        const uint32_t src = base + P::kOffS + s * P::kScales;
-        uint32_t a[4][P::kWords], b[P::kBCols][P::kWords];
+    while (lt < tiles) {
+      const int u = lu;
+      // stages before this unit
+      const uint32_t first =
+          (uint32_t)((lt - group) / groups) * steps + u * P::kUnitStages;
+      const int count = steps - u * P::kUnitStages < P::kUnitStages
+                            ? steps - u * P::kUnitStages
+                            : P::kUnitStages;
+      bar_sync(1 + turn, 128);  // the group has read its last unit
 #pragma unroll
-        for (int r = 0; r < 4 + NT / 32 + (NT < 32); ++r) {
-          const uint32_t at = src + (32 * r + lane) * P::kScaleRow;
-          uint32_t *v = r < 4 ? a[r] : b[r - 4];
-          if constexpr (P::kWords == 2)
-            asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];"
-                         : "=r"(v[0]), "=r"(v[1])
-                         : "r"(at));
-          else
-            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(v[0]), "=r"(v[1]), "=r"(v[P::kWords - 2]),
-                           "=r"(v[P::kWords - 1])
-                         : "r"(at));
-          if (FMT == TQ_FMT_NV4) {  // scales are read without a sign
-#pragma unroll
-            for (int w = 0; w < P::kWords; ++w) v[w] &= 0x7F7F7F7Fu;
-          }
-        }
-#pragma unroll
-        for (int r = NT / 32 + (NT < 32); r < (int)P::kBCols; ++r)
-#pragma unroll
-          for (int w = 0; w < P::kWords; ++w) b[r][w] = 0;
+      for (int j = 0; j < kRowsPer; ++j)
+        if (my_row + kPass * j < kRowsM + NT)
+          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(
+                           buf + scale_at<FMT, P::kUnit>(my_row + kPass * j,
+                                                         my_piece)),
+                       "r"(v[j].x), "r"(v[j].y)
+                       : "memory");
+      bar_sync(1 + turn, 128);
+      lu += kScaleGroups;
+      settle();
+      if (lt < tiles) load(lt, lu);
+#pragma unroll 1
+      for (int i = 0; i < count; ++i) {
+        const uint32_t it = first + i, s = it % S, ph = (it / S) & 1u;
         // the MMAs that read this slot's scales before are done; after a wait
-        // that gave up, the warps only keep meeting at the barrier above
+        // that gave up, the warps only keep meeting at the barriers above
         if (ok)
           ok = mbar_wait(empty + 8 * s, ph ^ 1u, abort_addr, kWaitLimitNs);
         ok = __all_sync(0xFFFFFFFFu, ok);
-        if (ok) {
-          tc_fence_after_sync();
-          const uint32_t sa = tmem_scales + s * P::kScaleCols + quarter;
-          const uint32_t sb = sa + P::kWords * 4;
+        if (!ok) continue;
+        tc_fence_after_sync();
+        const uint32_t cols = tmem_scales + s * P::kScaleCols + quarter;
+        const uint32_t piece = i * (P::kScaleRow / 8);
 #pragma unroll
-          for (int w = 0; w < P::kWords; ++w) {
-            tmem_st4(sa + 4 * w, a[0][w], a[1][w], a[2][w], a[3][w]);
+        for (int r0 = 0; r0 < 4 + (int)P::kBCols; r0 += 4) {
+          uint32_t a[4][4];
 #pragma unroll
-            for (int r = 0; r < (int)P::kBCols; r += 4)
-              tmem_st4(sb + P::kBCols * w + r, b[r][w], b[r + 1][w],
-                       b[r + 2][w], b[r + 3][w]);
+          for (int r = 0; r < 4; ++r) {
+            if (32 * (r0 + r) >= kRowsM + NT) {
+              a[r][0] = a[r][1] = a[r][2] = a[r][3] = 0;
+              continue;
+            }
+            const uint32_t at =
+                buf + scale_at<FMT, P::kUnit>(32 * (r0 + r) + lane, piece);
+            if constexpr (P::kWords == 2)
+              asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];"
+                           : "=r"(a[r][0]), "=r"(a[r][1])
+                           : "r"(at)
+                           : "memory");
+            else
+              asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                           : "=r"(a[r][0]), "=r"(a[r][1]), "=r"(a[r][2]),
+                             "=r"(a[r][3])
+                           : "r"(at)
+                           : "memory");
           }
-          tmem_st_wait();
-          tc_fence_before_sync();
-          // this CTA's codes are here as well
-          ok = mbar_wait(full + 8 * s, ph, abort_addr, kWaitLimitNs);
-          ok = __all_sync(0xFFFFFFFFu, ok);
-          if (ok && lane == 0) mbar_arrive_cluster(ready + 8 * s, 0);
+#pragma unroll
+          for (int w = 0; w < P::kWords; ++w)
+            tmem_st4(r0 == 0 ? cols + 4 * w
+                             : cols + P::kWords * 4 + P::kBCols * w + r0 - 4,
+                     a[0][w], a[1][w], a[2][w], a[3][w]);
         }
+        tmem_st_wait();
+        tc_fence_before_sync();
+        if (lane == 0) mbar_arrive(ready + 8 * s);
+        __syncwarp();
       }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (warp >= 8) {
-    const int q = warp & 3, half = (warp - 8) >> 2;  // lane quarter, columns
+  } else {
+    const int q = warp & 3, half = (warp - 10) >> 2;  // lane quarter, columns
     constexpr int kCols = NT / 2;
-    constexpr int kChunk = kCols < 16 ? 8 : 16;
     const float g = (args.wg != nullptr ? *args.wg : 1.0f) *
                     (args.xg != nullptr ? *args.xg : 1.0f);
+    // bf16 pairs need an even row pitch and a 4-byte aligned y
+    const bool pairs = args.y_bf16 && args.ldy % 2 == 0 && args.n % 2 == 0 &&
+                       (reinterpret_cast<uintptr_t>(args.y) & 3u) == 0;
     uint32_t done = 0;
     bool ok = true;
     for (int t = group; t < tiles; t += groups, ++done) {
-      if (ok) {
-        ok = mbar_wait(dfull, done & 1u, abort_addr, kWaitLimitNs);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-      }
+      if (ok) ok = mbar_wait(dfull, done & 1u, abort_addr, kWaitLimitNs);
+      ok = __all_sync(0xFFFFFFFFu, ok);
       tc_fence_after_sync();
       const int64_t row = (int64_t)(t / args.tiles_n) * (CG * kRowsM) +
                           rank * kRowsM + 32 * q + lane;
       const int64_t b0 = (int64_t)(t % args.tiles_n) * NT + half * kCols;
+      const int cols = (int)(args.batch - b0 < kCols ? args.batch - b0 : kCols);
       const uint32_t src = tmem + half * kCols + ((uint32_t)q << 21);
-#pragma unroll 1
-      for (int c = 0; c < kCols; c += kChunk) {
+      auto column16 = [&](int c, float (&f)[16]) {
         uint32_t v[16];
         if (ok) {
-          tmem_ld16(src + c, v);  // the last 8 of a chunk of 8 are not used
+          tmem_ld16(src + c, v);
           tmem_ld_wait();
-        } else {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) v[j] = 0x7FC00000u;
         }
-        if (row < args.n) {
 #pragma unroll
-          for (int j = 0; j < kChunk; ++j) {
-            const int64_t b = b0 + c + j;
-            const float f = __uint_as_float(v[j]) * g;
-            if (b < args.batch) {
-              if (args.y_bf16)
-                static_cast<__nv_bfloat16 *>(args.y)[b * args.ldy + row] =
-                    __float2bfloat16_rn(f);
-              else
-                static_cast<float *>(args.y)[b * args.ldy + row] = f;
-            }
+        for (int j = 0; j < 16; ++j)
+          f[j] = ok ? __uint_as_float(v[j]) * g : __int_as_float(0x7FC00000);
+      };
+      auto drained = [&]() {  // the accumulator may be written again
+        tc_fence_before_sync();
+        __syncwarp();
+        if (!ok || lane != 0) return;
+        if (CG == 2)
+          mbar_arrive_cluster(dempty, 0);
+        else
+          mbar_arrive(dempty);
+      };
+      if (args.y_bf16) {
+        // all columns first, as bf16 pairs (two columns of this lane's row),
+        // so that the next tile can start while they are stored
+        uint32_t h[kCols / 2];
+#pragma unroll
+        for (int c = 0; c < kCols; c += 16) {
+          float f[16];
+          column16(c, f);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const __nv_bfloat162 p =
+                __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
+            h[c / 2 + j] = *reinterpret_cast<const uint32_t *>(&p);
           }
         }
-        __syncwarp();
+        drained();
+        __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(args.y);
+        if (pairs) {
+          // lanes 2i and 2i + 1 swap, so that each stores two neighbouring
+          // rows of one column: the even lane column 2j, the odd lane 2j + 1
+          const int odd = lane & 1;
+          __nv_bfloat16 *p = y + (b0 + odd) * args.ldy + (row - odd);
+#pragma unroll
+          for (int j = 0; j < kCols / 2; ++j) {
+            const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, h[j], 1);
+            const uint32_t two =
+                odd ? __byte_perm(o, h[j], 0x7632) : __byte_perm(h[j], o, 0x5410);
+            if (row < args.n && 2 * j + odd < cols)
+              *reinterpret_cast<uint32_t *>(p) = two;
+            p += 2 * args.ldy;
+          }
+        } else if (row < args.n) {
+          __nv_bfloat16 *p = y + b0 * args.ldy + row;
+#pragma unroll
+          for (int j = 0; j < kCols; ++j) {
+            const uint32_t two = h[j / 2];
+            if (j < cols)
+              *p = __ushort_as_bfloat16(
+                  (unsigned short)(j & 1 ? two >> 16 : two));
+            p += args.ldy;
+          }
+        }
+      } else {
+        float *p = static_cast<float *>(args.y) + b0 * args.ldy + row;
+#pragma unroll 1
+        for (int c = 0; c < kCols; c += 16) {
+          float f[16];
+          column16(c, f);
+          if (row < args.n) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              if (c + j < cols) *p = f[j];
+              p += args.ldy;
+            }
+          }
+          __syncwarp();
+        }
+        drained();
       }
-      tc_fence_before_sync();
-      __syncwarp();
-      if (ok && lane == 0) mbar_arrive_cluster(dempty, 0);
     }
   }
 
@@ -453,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("barrier.cluster.arrive.aligned;\n"
                  "barrier.cluster.wait.aligned;" ::: "memory");
   }
-  if (warp == 2) {
+  if (warp == 0) {
     tc_fence_after_sync();
     free_columns<CG>(tmem, kTmemColumns);
   }
