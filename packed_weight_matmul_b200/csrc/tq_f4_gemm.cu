@@ -128,28 +128,37 @@ __device__ __forceinline__ void free_columns(uint32_t taddr, uint32_t cols) {
                  : "memory");
 }
 
-// Arrive on `bar` (of both CTAs of a pair) when all MMAs issued so far by
-// this thread are complete.
+// Arrive on `bar` (of both CTAs of a pair) when all MMAs issued so far are
+// complete. Whole warp; the elected lane is the one that issues the MMAs.
 template <int CG>
 __device__ __forceinline__ void commit(uint32_t bar) {
   if constexpr (CG == 1)
-    mma_commit(bar);
+    asm volatile(
+        "{\n .reg .pred q;\n elect.sync _|q, 0xFFFFFFFF;\n"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster."
+        "b64 [%0];\n}" ::"r"(bar)
+        : "memory");
   else
     asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster."
-        "multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "{\n .reg .pred q;\n elect.sync _|q, 0xFFFFFFFF;\n"
+        " @q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster."
+        "multicast::cluster.b64 [%0], %1;\n}" ::"r"(bar),
         "h"((uint16_t)3)
         : "memory");
 }
 
-// D (+)= (A * scale A)(B * scale B)^T over 64 k.
+// D (+)= (A * scale A)(B * scale B)^T over 64 k. The whole warp comes here
+// together and one elected lane issues: that way the operands stay in uniform
+// registers (issued from inside an `if (lane == 0)`, an MMA cost about 80
+// cycles of moving them there, more than the tensor core needed for it).
 template <int FMT, int CG>
 __device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b,
                                            uint32_t idesc, uint32_t sa,
                                            uint32_t sb, uint32_t accumulate) {
 #define TQ_MMA(GROUP, KIND)                                                   \
-  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"                  \
-               " tcgen05.mma.cta_group::" GROUP ".kind::" KIND                \
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %6, 0;\n"              \
+               " elect.sync _|q, 0xFFFFFFFF;\n"                               \
+               " @q tcgen05.mma.cta_group::" GROUP ".kind::" KIND             \
                " [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),               \
                "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)  \
                : "memory")
@@ -181,7 +190,6 @@ __device__ __forceinline__ void bar_sync(int id, int threads) {
 // 8 scale bytes of a row at `off`. Rows whose length is a multiple of 8 bytes
 // (k a multiple of 256) are read in one load, others byte by byte; bytes past
 // the row's end become 0 (their codes are zero too).
-template <int FMT>
 __device__ __forceinline__ uint2 load_scales8(const uint8_t *row, int row_bytes,
                                               int off, bool whole) {
   uint2 v = make_uint2(0u, 0u);
@@ -194,10 +202,6 @@ __device__ __forceinline__ uint2 load_scales8(const uint8_t *row, int row_bytes,
       if (off + 4 + b < row_bytes)
         v.y |= (uint32_t)__ldg(row + off + 4 + b) << (8 * b);
     }
-  }
-  if (FMT == TQ_FMT_NV4) {  // E4M3 scales are read without their sign
-    v.x &= 0x7F7F7F7Fu;
-    v.y &= 0x7F7F7F7Fu;
   }
   return v;
 }
@@ -213,6 +217,27 @@ __device__ __forceinline__ uint32_t scale_at(uint32_t r, uint32_t c) {
   return r * UNIT + 8u * (c ^ x);
 }
 
+// Two accumulator columns times g as bf16, `lo` in the low half.
+__device__ __forceinline__ uint32_t scaled_pair(uint32_t lo, uint32_t hi,
+                                                float g) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(lo) * g,
+                                                 __uint_as_float(hi) * g);
+  return *reinterpret_cast<const uint32_t *>(&p);
+}
+
+// Arrive on the barrier at this CTA's address `bar` in the pair's first CTA.
+// Relaxed: what it announces (bytes of completed tensor copies, completed
+// tensor-memory stores) is read by MMAs, not by loads that a release would
+// order, and this thread has waited for all of it.
+__device__ __forceinline__ void arrive_leader(uint32_t bar) {
+  uint32_t remote;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(remote) : "r"(bar));
+  asm volatile(
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+          remote)
+      : "memory");
+}
+
 template <int FMT, int NT, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
     product_f4_kernel(const __grid_constant__ CUtensorMap tmap_w,
@@ -224,10 +249,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t bars = base + P::kOffBar;
-  // ready: a stage's codes and scales are here; peer: those of the pair's
-  // second CTA; empty: its MMAs are done
-  const uint32_t ready = bars, peer = bars + 8 * S, empty = bars + 16 * S;
-  const uint32_t dfull = bars + 24 * S, dempty = dfull + 8;
+  // ready: a stage's codes and scales are here (in the first CTA of a pair:
+  // the second one's too); empty: its MMAs are done
+  const uint32_t ready = bars, empty = bars + 8 * S;
+  const uint32_t dfull = bars + 16 * S, dempty = dfull + 8;
   const uint32_t slot = dfull + 16, abort_addr = dfull + 20;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
   const int group = blockIdx.x / CG, groups = gridDim.x / CG;
@@ -236,8 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(ready + 8 * s, kScaleWarps + 1);
-      mbar_init(peer + 8 * s, 1);
+      mbar_init(ready + 8 * s, kScaleWarps + 1 + (CG == 2 && rank == 0));
       mbar_init(empty + 8 * s, 1);
     }
     mbar_init(dfull, 1);
@@ -253,8 +277,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                  "barrier.cluster.wait.aligned;" ::: "memory");
   }
   tc_fence_after_sync();
-  const uint32_t tmem = (uint32_t)ld_volatile_s32(slot);
-  const uint32_t tmem_scales = tmem + NT;
+  // all columns are this CTA's, so they start at column 0
+  constexpr uint32_t kTmem = 0;
+  constexpr uint32_t tmem_scales = kTmem + NT;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -286,36 +311,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < steps && ok; ++i, ++it) {
           ok = mbar_wait(ready + 8 * (it % S), (it / S) & 1u, abort_addr,
                          kWaitLimitNs);
-          if (ok) mbar_arrive_cluster(peer + 8 * (it % S), 0);
+          tc_fence_after_sync();
+          tc_fence_before_sync();
+          if (ok) arrive_leader(ready + 8 * (it % S));
         }
       }
     }
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {  // the whole warp, see mma_scaled
       uint32_t it = 0, done = 0;
       bool ok = true;
       for (int t = group; t < tiles && ok; t += groups, ++done) {
         if (done > 0)
           ok = mbar_wait_cluster(dempty, (done - 1) & 1u, abort_addr,
                                  kWaitLimitNs);
+        ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) break;
         for (int i = 0; i < steps; ++i, ++it) {
           const uint32_t s = it % S, ph = (it / S) & 1u;
-          ok = mbar_wait(ready + 8 * s, ph, abort_addr, kWaitLimitNs);
-          if (CG == 2)
-            ok = ok && mbar_wait_cluster(peer + 8 * s, ph, abort_addr,
-                                         kWaitLimitNs);
+          ok = CG == 2 ? mbar_wait_cluster(ready + 8 * s, ph, abort_addr,
+                                           kWaitLimitNs)
+                       : mbar_wait(ready + 8 * s, ph, abort_addr, kWaitLimitNs);
+          ok = __all_sync(0xFFFFFFFFu, ok);
           if (!ok) break;
           tc_fence_after_sync();
           const uint64_t a = smem_desc_kmajor_sw128(base + s * P::kA);
           const uint64_t b =
               smem_desc_kmajor_sw128(base + P::kOffB + s * P::kB);
-          const uint32_t sa = tmem_scales + s * P::kScaleCols;
+          const uint32_t sa = kTmem + NT + s * P::kScaleCols;
           const uint32_t sb = sa + P::kWords * 4;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int w = FMT == TQ_FMT_MX4 ? j / 2 : j;
             const uint32_t byte = FMT == TQ_FMT_MX4 ? (j & 1) * 2u : 0u;
-            mma_scaled<FMT, CG>(tmem, a + 2 * j, b + 2 * j,
+            mma_scaled<FMT, CG>(kTmem, a + 2 * j, b + 2 * j,
                                 idesc_f4<FMT>(CG * kRowsM, NT, byte),
                                 sa + 4 * w, sb + P::kBCols * w,
                                 (i | j) != 0 ? 1u : 0u);
@@ -341,22 +369,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kRowsPer = (kRowsM + NT + kPass - 1) / kPass;
     const int my_row = tid / kPieces, my_piece = tid % kPieces;
     uint2 v[kRowsPer];
-    // unit `lu` of tile `lt`, into registers
+    // unit `lu` of tile `lt`, into registers; rows past the matrix repeat the
+    // last one (their outputs are not stored)
+    int at_tile = -1;
+    const uint8_t *wrows = nullptr, *xrows = nullptr;
+    int wlast = 0, xlast = 0;
     auto load = [&](int lt, int lu) {
-      const int64_t m0 =
-          (int64_t)(lt / args.tiles_n) * (CG * kRowsM) + rank * kRowsM;
-      const int64_t b0 = (int64_t)(lt % args.tiles_n) * NT;
+      if (lt != at_tile) {
+        at_tile = lt;
+        const int64_t m0 =
+            (int64_t)(lt / args.tiles_n) * (CG * kRowsM) + rank * kRowsM;
+        const int64_t b0 = (int64_t)(lt % args.tiles_n) * NT;
+        const int64_t m = m0 < args.n ? m0 : args.n - 1;
+        wlast = (int)(args.n - 1 - m < kRowsM ? args.n - 1 - m : kRowsM);
+        xlast = (int)(args.batch - 1 - b0 < NT ? args.batch - 1 - b0 : NT);
+        wrows = args.wscales + m * row_bytes;
+        xrows = args.xscales + b0 * row_bytes;
+      }
       const int off = lu * (int)P::kUnit + 8 * my_piece;
 #pragma unroll
       for (int j = 0; j < kRowsPer; ++j) {
         const bool of_w = kPass * (j + 1) <= kRowsM;
-        const int64_t r = my_row + kPass * j;
-        int64_t at = of_w ? m0 + r : b0 + r - kRowsM;
-        const int64_t last = (of_w ? args.n : args.batch) - 1;
-        at = at < last ? at : last;
-        v[j] = load_scales8<FMT>(
-            (of_w ? args.wscales : args.xscales) + at * row_bytes, row_bytes,
-            off, whole);
+        int r = my_row + kPass * j - (of_w ? 0 : kRowsM);
+        r = min(r, of_w ? wlast : xlast);
+        v[j] = load_scales8((of_w ? wrows : xrows) + (int64_t)r * row_bytes,
+                            row_bytes, off, whole);
       }
     };
     // (tile, unit) of this group's next turn: every second unit in order
@@ -380,13 +417,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                             : P::kUnitStages;
       bar_sync(1 + turn, 128);  // the group has read its last unit
 #pragma unroll
-      for (int j = 0; j < kRowsPer; ++j)
+      for (int j = 0; j < kRowsPer; ++j) {
+        if (FMT == TQ_FMT_NV4) {  // E4M3 scales are read without their sign
+          v[j].x &= 0x7F7F7F7Fu;
+          v[j].y &= 0x7F7F7F7Fu;
+        }
         if (my_row + kPass * j < kRowsM + NT)
           asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(
                            buf + scale_at<FMT, P::kUnit>(my_row + kPass * j,
                                                          my_piece)),
                        "r"(v[j].x), "r"(v[j].y)
                        : "memory");
+      }
       bar_sync(1 + turn, 128);
       lu += kScaleGroups;
       settle();
@@ -456,40 +498,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                           rank * kRowsM + 32 * q + lane;
       const int64_t b0 = (int64_t)(t % args.tiles_n) * NT + half * kCols;
       const int cols = (int)(args.batch - b0 < kCols ? args.batch - b0 : kCols);
-      const uint32_t src = tmem + half * kCols + ((uint32_t)q << 21);
-      auto column16 = [&](int c, float (&f)[16]) {
-        uint32_t v[16];
-        if (ok) {
-          tmem_ld16(src + c, v);
-          tmem_ld_wait();
-        }
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-          f[j] = ok ? __uint_as_float(v[j]) * g : __int_as_float(0x7FC00000);
-      };
+      const uint32_t src = kTmem + half * kCols + ((uint32_t)q << 21);
+      const float gn = ok ? g : __int_as_float(0x7FC00000);
       auto drained = [&]() {  // the accumulator may be written again
         tc_fence_before_sync();
         __syncwarp();
         if (!ok || lane != 0) return;
         if (CG == 2)
-          mbar_arrive_cluster(dempty, 0);
+          arrive_leader(dempty);
         else
           mbar_arrive(dempty);
       };
+      // Chunks past the batch are left out; the branch also keeps a chunk's
+      // arithmetic behind its load (without it every column stayed in 32 bits
+      // until the end and was spilled: 4900 cycles for the 128 columns of a
+      // warp instead of 1150). As many columns as 64 registers hold are read first, so that the next
+      // tile can start while they are stored: all of them as bf16 pairs (two
+      // columns of this lane's row), 64 in fp32.
+      uint32_t h[kCols / 2 < 16 ? 16 : kCols / 2] = {};
       if (args.y_bf16) {
-        // all columns first, as bf16 pairs (two columns of this lane's row),
-        // so that the next tile can start while they are stored
-        uint32_t h[kCols / 2];
 #pragma unroll
         for (int c = 0; c < kCols; c += 16) {
-          float f[16];
-          column16(c, f);
+          if (c >= cols) break;
+          uint32_t v[16];
+          tmem_ld16(src + c, v);
+          tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const __nv_bfloat162 p =
-                __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
-            h[c / 2 + j] = *reinterpret_cast<const uint32_t *>(&p);
-          }
+          for (int j = 0; j < 8; ++j)
+            h[c / 2 + j] = scaled_pair(v[2 * j], v[2 * j + 1], gn);
         }
         drained();
         __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(args.y);
@@ -519,21 +555,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       } else {
+        constexpr int kHeld = kCols / 2 < 16 ? 16 : kCols / 2;
         float *p = static_cast<float *>(args.y) + b0 * args.ldy + row;
 #pragma unroll 1
-        for (int c = 0; c < kCols; c += 16) {
-          float f[16];
-          column16(c, f);
+        for (int c = 0; c < kCols; c += kHeld) {
+#pragma unroll
+          for (int i = 0; i < kHeld; i += 16) {
+            if (c + i >= cols) break;
+            uint32_t v[16];
+            tmem_ld16(src + c + i, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              h[i + j] = __float_as_uint(__uint_as_float(v[j]) * gn);
+          }
+          if (c + kHeld >= kCols) drained();
           if (row < args.n) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              if (c + j < cols) *p = f[j];
+            for (int j = 0; j < kHeld; ++j) {
+              if (c + j < cols) *p = __uint_as_float(h[j]);
               p += args.ldy;
             }
           }
           __syncwarp();
         }
-        drained();
       }
     }
   }
@@ -547,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 0) {
     tc_fence_after_sync();
-    free_columns<CG>(tmem, kTmemColumns);
+    free_columns<CG>(kTmem, kTmemColumns);
   }
 }
 
@@ -634,7 +679,7 @@ cudaError_t dispatch(const WeightsView &w, const WeightsView &x, void *y,
   if (x.n <= 32) return launch<FMT, 32, 1>(w, x, y, ldy, y_type, stream);
   if (x.n <= 64) return launch<FMT, 64, 1>(w, x, y, ldy, y_type, stream);
   if (x.n <= 128) return launch<FMT, 128, 1>(w, x, y, ldy, y_type, stream);
-  return launch<FMT, 256, 1>(w, x, y, ldy, y_type, stream);
+  return launch<FMT, 256, 2>(w, x, y, ldy, y_type, stream);
 }
 
 }  // namespace
