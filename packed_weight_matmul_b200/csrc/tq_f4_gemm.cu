@@ -20,8 +20,8 @@
 //   warp 1       MMA issuer (first CTA of a pair): 4 MMAs of K = 64 per stage;
 //                in the second CTA it passes "stage ready" on to the first
 //   warps 2-9    scales, two groups of four warps that take turns. A group
-//                reads 32 bytes of scales of every row (one sector; 4 stages of
-//                MX4, 2 of NV4) into registers one turn ahead, lays them down
+//                reads the scales of every row for 4 stages (32 bytes of MX4,
+//                64 of NV4) into registers one turn ahead, lays them down
 //                row by row in shared memory, and then per stage every warp
 //                reads rows lane, lane + 32, ... and stores word w of row group
 //                i to column 4 w + i of its own lane quarter, which is the
@@ -59,13 +59,14 @@ struct Plan {
   static constexpr uint32_t kA = kRowsM * kStageRow;
   static constexpr uint32_t kB = (NT / CG) * kStageRow;
   static constexpr uint32_t kStage = kA + kB;
-  // scale bytes of a row that a group reads at once: a 32-byte sector where
-  // the ring is long enough (see the assertion below)
+  // scale bytes of a row that a group reads at once, four pieces of one load
+  // each where the ring is long enough (see the assertion below), else two
+  static constexpr uint32_t kPiece = FMT == TQ_FMT_NV4 ? 16u : 8u;
   static constexpr uint32_t kUnit =
-      FMT == TQ_FMT_NV4 || 5 * kStage + 2 * (kRowsM + NT) * 32u + 3072u <=
-                               kSmemLimit
-          ? 32u
-          : 16u;
+      kPiece * (5 * kStage + 2 * (kRowsM + NT) * 4 * kPiece + 3072u <=
+                        kSmemLimit
+                    ? 4u
+                    : 2u);
   static constexpr int kUnitStages = (int)(kUnit / kScaleRow);
   static constexpr uint32_t kScales = (kRowsM + NT) * kUnit;  // of one group
   static constexpr int kFit =
@@ -187,34 +188,56 @@ __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// 8 scale bytes of a row at `off`. Rows whose length is a multiple of 8 bytes
-// (k a multiple of 256) are read in one load, others byte by byte; bytes past
-// the row's end become 0 (their codes are zero too).
-__device__ __forceinline__ uint2 load_scales8(const uint8_t *row, int row_bytes,
-                                              int off, bool whole) {
-  uint2 v = make_uint2(0u, 0u);
+// One piece (8 or 16 scale bytes) of a row at `off`. Rows whose length is a
+// multiple of it (k a multiple of 256) are read in one load, others byte by
+// byte; bytes past the row's end become 0 (their codes are zero too).
+template <int WORDS>
+__device__ __forceinline__ void load_piece(uint32_t (&v)[WORDS],
+                                           const uint8_t *row, int row_bytes,
+                                           int off, bool whole) {
+#pragma unroll
+  for (int w = 0; w < WORDS; ++w) v[w] = 0;
   if (whole) {
-    if (off < row_bytes) v = __ldg(reinterpret_cast<const uint2 *>(row + off));
+    if (off >= row_bytes) return;
+    if constexpr (WORDS == 2) {
+      const uint2 t = __ldg(reinterpret_cast<const uint2 *>(row + off));
+      v[0] = t.x;
+      v[1] = t.y;
+    } else {
+      const uint4 t = __ldg(reinterpret_cast<const uint4 *>(row + off));
+      v[0] = t.x;
+      v[1] = t.y;
+      v[2] = t.z;
+      v[3] = t.w;
+    }
   } else {
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      if (off + b < row_bytes) v.x |= (uint32_t)__ldg(row + off + b) << (8 * b);
-      if (off + 4 + b < row_bytes)
-        v.y |= (uint32_t)__ldg(row + off + 4 + b) << (8 * b);
-    }
+    for (int b = 0; b < 4 * WORDS; ++b)
+      if (off + b < row_bytes)
+        v[b / 4] |= (uint32_t)__ldg(row + off + b) << (8 * (b % 4));
   }
-  return v;
 }
 
-// Where byte 8 c of row r's unit lies in a group's scale buffer: rows UNIT
-// bytes apart, the 8-byte (MX4) or 16-byte (NV4) pieces of a row swapped so
-// that the reads of one piece by 32 consecutive rows hit different banks.
-template <int FMT, uint32_t UNIT>
+template <int WORDS>
+__device__ __forceinline__ void store_piece(uint32_t at,
+                                            const uint32_t (&v)[WORDS]) {
+  if constexpr (WORDS == 2)
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(v[0]),
+                 "r"(v[1])
+                 : "memory");
+  else
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at),
+                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                 : "memory");
+}
+
+// Where piece c of row r's unit (PIECES of BYTES bytes) lies in a group's
+// scale buffer: row after row, a row's pieces swapped so that the reads of
+// one piece by consecutive rows hit different banks.
+template <uint32_t PIECES, uint32_t BYTES>
 __device__ __forceinline__ uint32_t scale_at(uint32_t r, uint32_t c) {
-  const uint32_t x = FMT == TQ_FMT_NV4 ? ((r >> 2) & 1u) << 1
-                     : UNIT == 32u     ? (r >> 2) & 3u
-                                       : (r >> 3) & 1u;
-  return r * UNIT + 8u * (c ^ x);
+  constexpr uint32_t kRowsPer128 = 128u / (PIECES * BYTES);
+  return (r * PIECES + (c ^ ((r / kRowsPer128) & (PIECES - 1)))) * BYTES;
 }
 
 // Two accumulator columns times g as bf16, `lo` in the low half.
@@ -364,11 +387,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool whole = args.k % 256 == 0;
     const uint32_t buf = base + P::kOffS + turn * P::kScales;
     const int units = (steps + P::kUnitStages - 1) / P::kUnitStages;
-    // a row's unit is read by kUnit / 8 neighbouring threads
-    constexpr int kPieces = (int)P::kUnit / 8, kPass = 128 / kPieces;
+    // a row's unit is read by kPieces neighbouring threads
+    constexpr int kPieces = (int)(P::kUnit / P::kPiece), kPass = 128 / kPieces;
+    constexpr int kPieceWords = (int)P::kPiece / 4;
     constexpr int kRowsPer = (kRowsM + NT + kPass - 1) / kPass;
     const int my_row = tid / kPieces, my_piece = tid % kPieces;
-    uint2 v[kRowsPer];
+    uint32_t v[kRowsPer][kPieceWords];
     // unit `lu` of tile `lt`, into registers; rows past the matrix repeat the
     // last one (their outputs are not stored)
     int at_tile = -1;
@@ -386,14 +410,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         wrows = args.wscales + m * row_bytes;
         xrows = args.xscales + b0 * row_bytes;
       }
-      const int off = lu * (int)P::kUnit + 8 * my_piece;
+      const int off = lu * (int)P::kUnit + (int)P::kPiece * my_piece;
 #pragma unroll
       for (int j = 0; j < kRowsPer; ++j) {
         const bool of_w = kPass * (j + 1) <= kRowsM;
         int r = my_row + kPass * j - (of_w ? 0 : kRowsM);
         r = min(r, of_w ? wlast : xlast);
-        v[j] = load_scales8((of_w ? wrows : xrows) + (int64_t)r * row_bytes,
-                            row_bytes, off, whole);
+        load_piece(v[j], (of_w ? wrows : xrows) + (int64_t)r * row_bytes,
+                   row_bytes, off, whole);
       }
     };
     // (tile, unit) of this group's next turn: every second unit in order
@@ -419,15 +443,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int j = 0; j < kRowsPer; ++j) {
         if (FMT == TQ_FMT_NV4) {  // E4M3 scales are read without their sign
-          v[j].x &= 0x7F7F7F7Fu;
-          v[j].y &= 0x7F7F7F7Fu;
+#pragma unroll
+          for (int w = 0; w < kPieceWords; ++w) v[j][w] &= 0x7F7F7F7Fu;
         }
         if (my_row + kPass * j < kRowsM + NT)
-          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(
-                           buf + scale_at<FMT, P::kUnit>(my_row + kPass * j,
-                                                         my_piece)),
-                       "r"(v[j].x), "r"(v[j].y)
-                       : "memory");
+          store_piece(buf + scale_at<kPieces, P::kPiece>(my_row + kPass * j,
+                                                         my_piece),
+                      v[j]);
       }
       bar_sync(1 + turn, 128);
       lu += kScaleGroups;
@@ -444,7 +466,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) continue;
         tc_fence_after_sync();
         const uint32_t cols = tmem_scales + s * P::kScaleCols + quarter;
-        const uint32_t piece = i * (P::kScaleRow / 8);
 #pragma unroll
         for (int r0 = 0; r0 < 4 + (int)P::kBCols; r0 += 4) {
           uint32_t a[4][4];
@@ -455,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               continue;
             }
             const uint32_t at =
-                buf + scale_at<FMT, P::kUnit>(32 * (r0 + r) + lane, piece);
+                buf + scale_at<kPieces, P::kPiece>(32 * (r0 + r) + lane, i);
             if constexpr (P::kWords == 2)
               asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];"
                            : "=r"(a[r][0]), "=r"(a[r][1])
