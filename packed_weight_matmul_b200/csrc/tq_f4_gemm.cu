@@ -129,48 +129,99 @@ __device__ __forceinline__ void free_columns(uint32_t taddr, uint32_t cols) {
                  : "memory");
 }
 
+// Whether the phase of parity `parity` is over, without waiting; for a pair
+// with acquire at cluster scope.
+template <int CG>
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  if constexpr (CG == 1)
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], "
+        "%2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+  return ok != 0;
+}
+
+#define TQ_COMMIT_1                                                          \
+  "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64"
+#define TQ_COMMIT_2                                                          \
+  "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster."       \
+  "multicast::cluster.b64"
+
 // Arrive on `bar` (of both CTAs of a pair) when all MMAs issued so far are
 // complete. Whole warp; the elected lane is the one that issues the MMAs.
 template <int CG>
 __device__ __forceinline__ void commit(uint32_t bar) {
   if constexpr (CG == 1)
-    asm volatile(
-        "{\n .reg .pred q;\n elect.sync _|q, 0xFFFFFFFF;\n"
-        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster."
-        "b64 [%0];\n}" ::"r"(bar)
-        : "memory");
+    asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xFFFFFFFF;\n"
+                 " @q " TQ_COMMIT_1 " [%0];\n}" ::"r"(bar)
+                 : "memory");
   else
-    asm volatile(
-        "{\n .reg .pred q;\n elect.sync _|q, 0xFFFFFFFF;\n"
-        " @q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster."
-        "multicast::cluster.b64 [%0], %1;\n}" ::"r"(bar),
-        "h"((uint16_t)3)
-        : "memory");
+    asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xFFFFFFFF;\n"
+                 " @q " TQ_COMMIT_2 " [%0], %1;\n}" ::"r"(bar),
+                 "h"((uint16_t)3)
+                 : "memory");
 }
 
-// D (+)= (A * scale A)(B * scale B)^T over 64 k. The whole warp comes here
-// together and one elected lane issues: that way the operands stay in uniform
-// registers (issued from inside an `if (lane == 0)`, an MMA cost about 80
-// cycles of moving them there, more than the tensor core needed for it).
+// One stage: D (+)= (A * scale A)(B * scale B)^T over 4 x 64 k, then arrive
+// on `bar` as commit does. id0 / id1 are the instruction descriptors of even
+// and odd MMAs, whose scale words start at sa + 4 w and sb + bcols w, w = j
+// (NV4) or j / 2 (MX4). The whole warp comes here together and one elected
+// lane issues: that way the operands stay in uniform registers (issued from
+// inside an `if (lane == 0)`, an MMA cost about 80 cycles of moving them
+// there, more than the tensor core needed for it).
 template <int FMT, int CG>
-__device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t a, uint64_t b,
-                                           uint32_t idesc, uint32_t sa,
-                                           uint32_t sb, uint32_t accumulate) {
-#define TQ_MMA(GROUP, KIND)                                                   \
-  asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %6, 0;\n"              \
-               " elect.sync _|q, 0xFFFFFFFF;\n"                               \
-               " @q tcgen05.mma.cta_group::" GROUP ".kind::" KIND             \
-               " [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(d),               \
-               "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)  \
-               : "memory")
+__device__ __forceinline__ void mma_stage(uint32_t d, uint64_t a, uint64_t b,
+                                          uint32_t id0, uint32_t id1,
+                                          uint32_t sa, uint32_t sb,
+                                          uint32_t bcols, uint32_t accumulate,
+                                          uint32_t bar) {
+  constexpr uint32_t kW = FMT == TQ_FMT_NV4 ? 1u : 0u;
+  const uint32_t sa1 = sa + 4 * kW, sb1 = sb + bcols * kW;
+  const uint32_t sa2 = sa + 4 * (1 + kW), sb2 = sb + bcols * (1 + kW);
+  const uint32_t sa3 = sa2 + 4 * kW, sb3 = sb2 + bcols * kW;
+#define TQ_MMA(KIND, DA, DB, ID, SA, SB, P)                                   \
+  " @q tcgen05.mma.cta_group::" KIND " [%0], " DA ", " DB ", " ID ", [" SA     \
+  "], [" SB "], " P ";\n"
+#define TQ_STAGE(KIND, COMMIT)                                                \
+  asm volatile(                                                               \
+      "{\n .reg .pred p, q, t;\n .reg .b64 a1, a2, a3, b1, b2, b3;\n"         \
+      " elect.sync _|q, 0xFFFFFFFF;\n setp.ne.b32 p, %13, 0;\n"               \
+      " setp.eq.b32 t, 0, 0;\n"                                               \
+      " add.s64 a1, %1, 2;\n add.s64 a2, %1, 4;\n add.s64 a3, %1, 6;\n"       \
+      " add.s64 b1, %2, 2;\n add.s64 b2, %2, 4;\n add.s64 b3, %2, 6;\n"       \
+      TQ_MMA(KIND, "%1", "%2", "%3", "%5", "%9", "p")                         \
+      TQ_MMA(KIND, "a1", "b1", "%4", "%6", "%10", "t")                        \
+      TQ_MMA(KIND, "a2", "b2", "%3", "%7", "%11", "t")                        \
+      TQ_MMA(KIND, "a3", "b3", "%4", "%8", "%12", "t")                        \
+      " @q " COMMIT ";\n}" ::"r"(d),                                          \
+      "l"(a), "l"(b), "r"(id0), "r"(id1), "r"(sa), "r"(sa1), "r"(sa2),        \
+      "r"(sa3), "r"(sb), "r"(sb1), "r"(sb2), "r"(sb3), "r"(accumulate),       \
+      "r"(bar), "h"((uint16_t)3)                                              \
+      : "memory")
   if constexpr (FMT == TQ_FMT_MX4 && CG == 1)
-    TQ_MMA("1", "mxf4.block_scale.scale_vec::2X");
+    TQ_STAGE("1.kind::mxf4.block_scale.scale_vec::2X", TQ_COMMIT_1 " [%14]");
   else if constexpr (FMT == TQ_FMT_MX4)
-    TQ_MMA("2", "mxf4.block_scale.scale_vec::2X");
+    TQ_STAGE("2.kind::mxf4.block_scale.scale_vec::2X",
+             TQ_COMMIT_2 " [%14], %15");
   else if constexpr (CG == 1)
-    TQ_MMA("1", "mxf4nvf4.block_scale.scale_vec::4X");
+    TQ_STAGE("1.kind::mxf4nvf4.block_scale.scale_vec::4X",
+             TQ_COMMIT_1 " [%14]");
   else
-    TQ_MMA("2", "mxf4nvf4.block_scale.scale_vec::4X");
+    TQ_STAGE("2.kind::mxf4nvf4.block_scale.scale_vec::4X",
+             TQ_COMMIT_2 " [%14], %15");
+#undef TQ_STAGE
 #undef TQ_MMA
 }
 
@@ -188,33 +239,38 @@ __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// One piece (8 or 16 scale bytes) of a row at `off`. Rows whose length is a
-// multiple of it (k a multiple of 256) are read in one load, others byte by
-// byte; bytes past the row's end become 0 (their codes are zero too).
+// One piece (8 or 16 scale bytes) of a row at `off`, `left` bytes before the
+// row's end; bytes past it are 0 (their codes are zero too).
 template <int WORDS>
 __device__ __forceinline__ void load_piece(uint32_t (&v)[WORDS],
-                                           const uint8_t *row, int row_bytes,
-                                           int off, bool whole) {
+                                           const uint8_t *p, int left) {
 #pragma unroll
   for (int w = 0; w < WORDS; ++w) v[w] = 0;
-  if (whole) {
-    if (off >= row_bytes) return;
-    if constexpr (WORDS == 2) {
-      const uint2 t = __ldg(reinterpret_cast<const uint2 *>(row + off));
-      v[0] = t.x;
-      v[1] = t.y;
-    } else {
-      const uint4 t = __ldg(reinterpret_cast<const uint4 *>(row + off));
-      v[0] = t.x;
-      v[1] = t.y;
-      v[2] = t.z;
-      v[3] = t.w;
-    }
+  if (left <= 0) return;
+  if constexpr (WORDS == 2) {
+    const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p));
+    v[0] = u.x;
+    v[1] = u.y;
   } else {
+    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
+    v[0] = u.x;
+    v[1] = u.y;
+    v[2] = u.z;
+    v[3] = u.w;
+  }
+}
+
+// The same byte by byte, for rows that do not start on a piece's boundary.
+template <int WORDS>
+__device__ __forceinline__ void load_piece_bytes(uint32_t (&v)[WORDS],
+                                                 const uint8_t *p, int left) {
 #pragma unroll
-    for (int b = 0; b < 4 * WORDS; ++b)
-      if (off + b < row_bytes)
-        v[b / 4] |= (uint32_t)__ldg(row + off + b) << (8 * (b % 4));
+  for (int w = 0; w < WORDS; ++w) {
+    uint32_t x = 0;
+#pragma unroll 1
+    for (int b = 0; b < 4 && 4 * w + b < left; ++b)
+      x |= (uint32_t)__ldg(p + 4 * w + b) << (8 * b);
+    v[w] = x;
   }
 }
 
@@ -282,6 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tiles = args.tiles_m * args.tiles_n;
   const int steps = (args.k + 255) / 256;
 
+  pdl_launch_dependents();
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(ready + 8 * s, kScaleWarps + 1 + (CG == 2 && rank == 0));
@@ -300,6 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                  "barrier.cluster.wait.aligned;" ::: "memory");
   }
   tc_fence_after_sync();
+  pdl_wait();  // user memory is read and written from here on
   // all columns are this CTA's, so they start at column 0
   constexpr uint32_t kTmem = 0;
   constexpr uint32_t tmem_scales = kTmem + NT;
@@ -342,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (rank == 0) {  // the whole warp, see mma_scaled
       uint32_t it = 0, done = 0;
-      bool ok = true;
+      bool ok = true, here = false;
       for (int t = group; t < tiles && ok; t += groups, ++done) {
         if (done > 0)
           ok = mbar_wait_cluster(dempty, (done - 1) & 1u, abort_addr,
@@ -351,27 +409,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         for (int i = 0; i < steps; ++i, ++it) {
           const uint32_t s = it % S, ph = (it / S) & 1u;
-          ok = CG == 2 ? mbar_wait_cluster(ready + 8 * s, ph, abort_addr,
-                                           kWaitLimitNs)
-                       : mbar_wait(ready + 8 * s, ph, abort_addr, kWaitLimitNs);
-          ok = __all_sync(0xFFFFFFFFu, ok);
-          if (!ok) break;
-          tc_fence_after_sync();
-          const uint64_t a = smem_desc_kmajor_sw128(base + s * P::kA);
-          const uint64_t b =
-              smem_desc_kmajor_sw128(base + P::kOffB + s * P::kB);
-          const uint32_t sa = kTmem + NT + s * P::kScaleCols;
-          const uint32_t sb = sa + P::kWords * 4;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int w = FMT == TQ_FMT_MX4 ? j / 2 : j;
-            const uint32_t byte = FMT == TQ_FMT_MX4 ? (j & 1) * 2u : 0u;
-            mma_scaled<FMT, CG>(kTmem, a + 2 * j, b + 2 * j,
-                                idesc_f4<FMT>(CG * kRowsM, NT, byte),
-                                sa + 4 * w, sb + P::kBCols * w,
-                                (i | j) != 0 ? 1u : 0u);
+          if (!here) {
+            ok = CG == 2 ? mbar_wait_cluster(ready + 8 * s, ph, abort_addr,
+                                             kWaitLimitNs)
+                         : mbar_wait(ready + 8 * s, ph, abort_addr,
+                                     kWaitLimitNs);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
           }
-          commit<CG>(empty + 8 * s);
+          tc_fence_after_sync();
+          // the next stage's barrier is asked before this one's MMAs go out (by
+          // a test that never suspends the warp, as try_wait may)
+          const uint32_t s1 = (it + 1) % S, ph1 = ((it + 1) / S) & 1u;
+          const bool next = mbar_test<CG>(ready + 8 * s1, ph1);
+          const uint32_t sa = kTmem + NT + s * P::kScaleCols;
+          mma_stage<FMT, CG>(
+              kTmem, smem_desc_kmajor_sw128(base + s * P::kA),
+              smem_desc_kmajor_sw128(base + P::kOffB + s * P::kB),
+              idesc_f4<FMT>(CG * kRowsM, NT, 0u),
+              idesc_f4<FMT>(CG * kRowsM, NT, FMT == TQ_FMT_MX4 ? 2u : 0u), sa,
+              sa + P::kWords * 4, P::kBCols, i != 0 ? 1u : 0u, empty + 8 * s);
+          here = __all_sync(0xFFFFFFFFu, next);
         }
         if (ok) commit<CG>(dfull);
       }
@@ -411,14 +469,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         xrows = args.xscales + b0 * row_bytes;
       }
       const int off = lu * (int)P::kUnit + (int)P::kPiece * my_piece;
+      auto each = [&](auto read) {
 #pragma unroll
-      for (int j = 0; j < kRowsPer; ++j) {
-        const bool of_w = kPass * (j + 1) <= kRowsM;
-        int r = my_row + kPass * j - (of_w ? 0 : kRowsM);
-        r = min(r, of_w ? wlast : xlast);
-        load_piece(v[j], (of_w ? wrows : xrows) + (int64_t)r * row_bytes,
-                   row_bytes, off, whole);
-      }
+        for (int j = 0; j < kRowsPer; ++j) {
+          const bool of_w = kPass * (j + 1) <= kRowsM;
+          int r = my_row + kPass * j - (of_w ? 0 : kRowsM);
+          r = min(r, of_w ? wlast : xlast);
+          read(v[j], (of_w ? wrows : xrows) + (int64_t)r * row_bytes + off);
+        }
+      };
+      // rows whose length is a multiple of a piece (k a multiple of 256)
+      // start on its boundary
+      if (whole)
+        each([&](uint32_t (&d)[kPieceWords], const uint8_t *p) {
+          load_piece(d, p, row_bytes - off);
+        });
+      else
+        each([&](uint32_t (&d)[kPieceWords], const uint8_t *p) {
+          load_piece_bytes(d, p, row_bytes - off);
+        });
     };
     // (tile, unit) of this group's next turn: every second unit in order
     int lt = group, lu = turn;
@@ -684,13 +753,15 @@ cudaError_t launch(const WeightsView &w, const WeightsView &x, void *y,
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = P::kSmem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = CG;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CG;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = CG == 1 ? 1 : 2;
   return cudaLaunchKernelEx(&cfg, kern, mw, mx, a);
 }
 
@@ -699,8 +770,22 @@ cudaError_t dispatch(const WeightsView &w, const WeightsView &x, void *y,
                      int64_t ldy, int y_type, cudaStream_t stream) {
   if (x.n <= 32) return launch<FMT, 32, 1>(w, x, y, ldy, y_type, stream);
   if (x.n <= 64) return launch<FMT, 64, 1>(w, x, y, ldy, y_type, stream);
-  if (x.n <= 128) return launch<FMT, 128, 1>(w, x, y, ldy, y_type, stream);
-  return launch<FMT, 256, 2>(w, x, y, ldy, y_type, stream);
+  // A wave of 256 x 256 tiles takes 7/5 of the time of a wave of 128 x 128
+  // tiles, two of which cover half of it (measured per 32 stages on 148 SMs:
+  // 14.1 and 10.1 us), so the large tile wins where its waves are full: 98
+  // against 129 us at 21504 x 5376 x 2048 rows, but 38 against 29 us at
+  // 5376 x 8192 x 777 rows (84 tiles on 74 pairs).
+  int dev = 0, sms = 148;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  auto waves = [&](int64_t m, int64_t b, int64_t at_once) {
+    const int64_t tiles = ((w.n + m - 1) / m) * ((x.n + b - 1) / b);
+    return (tiles + at_once - 1) / at_once;
+  };
+  if (x.n > 128 && 7 * waves(256, 256, sms / 2) <= 5 * waves(128, 128, sms))
+    return launch<FMT, 256, 2>(w, x, y, ldy, y_type, stream);
+  return launch<FMT, 128, 1>(w, x, y, ldy, y_type, stream);
 }
 
 }  // namespace
