@@ -60,7 +60,11 @@ cudaError_t launch_linear_experts_f4(const WeightsView &w, int n_experts,
                                      const __nv_bfloat16 *x, int64_t ldx,
                                      float *y, int64_t ldy, int32_t *status,
                                      cudaStream_t stream);
-// y = x W^T, both in 4 bits.
+// y = x W^T, both in 4 bits: up to 16 rows of x on the row kernel, more on the
+// block-scaled tensor cores.
+bool rows_f4_packed_supported(const WeightsView &x);
+cudaError_t rows_f4_packed(const WeightsView &w, const WeightsView &x, void *y,
+                           int64_t ldy, int y_type, cudaStream_t stream);
 cudaError_t launch_linear_f4(const WeightsView &w, const WeightsView &x,
                              void *y, int64_t ldy, int y_type,
                              cudaStream_t stream);

@@ -793,6 +793,8 @@ cudaError_t dispatch(const WeightsView &w, const WeightsView &x, void *y,
 cudaError_t launch_linear_f4(const WeightsView &w, const WeightsView &x,
                              void *y, int64_t ldy, int y_type,
                              cudaStream_t stream) {
+  if (rows_f4_packed_supported(x))
+    return rows_f4_packed(w, x, y, ldy, y_type, stream);
   return w.format == TQ_FMT_MX4
              ? dispatch<TQ_FMT_MX4>(w, x, y, ldy, y_type, stream)
              : dispatch<TQ_FMT_NV4>(w, x, y, ldy, y_type, stream);

@@ -1,0 +1,71 @@
+// Shared by the row products with 4-bit weights (tq_f4_linear.cu).
+#pragma once
+
+#include "tq_f4.cuh"
+#include "tq_sm100_async.cuh"
+
+namespace tq {
+
+// Two fp16 products.
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// D += A B, A 16 x 16 fp16 (rows g and g + 8 of lane 4 g + t), B 16 x 8 fp16
+// (column g), D 16 x 8 fp32 (rows g, g + 8; columns 2 t, 2 t + 1).
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
+                                        uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
+      "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// `bytes` (4, 8 or 16) from global to shared memory, or as many zeros.
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void *src,
+                                         bool live) {
+  const int n = live ? BYTES : 0;
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
+                 "l"(src), "r"(n)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst),
+                 "l"(src), "n"(BYTES), "r"(n)
+                 : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
+}
+
+__device__ __forceinline__ uint32_t lds_u8(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void sts128(uint32_t at, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x),
+               "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+
+// fp32 2^e for e <= 0, at least 2^-126: a factor for sums that are scaled down
+// (never 0, so that an infinite sum stays infinite; what is left of a finite
+// one is far below the resolution of the sum it is added to).
+__device__ __forceinline__ float pow2_down(int e) {
+  return __uint_as_float((uint32_t)((e < -126 ? -126 : e) + 127) << 23);
+}
+
+}  // namespace tq
