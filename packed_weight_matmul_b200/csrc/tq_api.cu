@@ -92,6 +92,8 @@ tq_status check_weights(const tq_weights *w, tq::WeightsView *v) {
     if (!aligned(w->codes, 16) || !aligned(w->scales, 16) ||
         !aligned(w->lut, 4))
       return TQ_ERR_ALIGNMENT;
+    // 16 rows of codes are addressed by 32-bit offsets
+    if (w->k_cols > (1 << 27)) return TQ_ERR_UNSUPPORTED;
     v->group = block;
   } else {
     return TQ_ERR_INVALID_ARG;
@@ -253,8 +255,8 @@ tq_status tq_linear_f4(const tq_weights *w, const tq_weights *x, void *y,
   if (y_type != TQ_Y_F32 && y_type != TQ_Y_BF16) return TQ_ERR_INVALID_ARG;
   if (u.k != v.k || ldy < v.n) return TQ_ERR_SHAPE;
   if (!aligned(y, y_type == TQ_Y_F32 ? 4 : 2)) return TQ_ERR_ALIGNMENT;
-  // row and column indices of the tensor copies are 32-bit
-  if (v.n > INT32_MAX / 2 || u.n > INT32_MAX / 2 || v.k > INT32_MAX / 2)
+  // row indices of the tensor copies are 32-bit
+  if (v.n > INT32_MAX / 2 || u.n > INT32_MAX / 2)
     return TQ_ERR_UNSUPPORTED;
   if (v.n == 0 || u.n == 0) return TQ_OK;
   cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);

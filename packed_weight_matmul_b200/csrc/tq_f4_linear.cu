@@ -33,6 +33,7 @@
 // takes 16 consecutive bytes (32 codes) of rows g and g + 8, and its part of
 // an x row is the same 32 k, 8 per 16-byte load.
 #include <cooperative_groups.h>
+#include <stdlib.h>
 
 #include "tq_f4_rows.cuh"
 
@@ -42,7 +43,9 @@ namespace {
 constexpr int kStageK = 256;    // codes of a row per stage
 constexpr int kRing = 3;        // stages of a warp's ring
 constexpr int kSegment = 2048;  // ids looked through at once
+constexpr int kPrefetch = 1024; // bytes of a row hinted to the L2 cache
 
+static int g_force_ks = getenv("FORCE_KS") ? atoi(getenv("FORCE_KS")) : 0;
 // Where the rows of x come from.
 enum { kBf16 = 0, kPacked = 1 };
 
@@ -78,8 +81,9 @@ struct RowPlan {
   static constexpr int kXStages = kXK / kStageK;
   static constexpr int kXPitch = kXK * 2 + 64;
   static constexpr int kXBuf = NT * kXPitch;
-  static constexpr int kPerWarp = NT / kWarps;  // rows of x a warp stages
-  static constexpr int kUnits = kXK / 256;      // 8-value units per lane
+  static constexpr int kUnits = kXK / 8;  // 8-value units of a buffered x row
+  static constexpr int kPer = NT * kUnits / kThreads;  // units per thread
+  static_assert(kUnits % 32 == 0 && kPer == 4, "a warp's units share a row");
   static constexpr int kPartPitch = kTile + 4;
   static constexpr int kRingBytes = kWarps * kRing * kStage;
   static constexpr int kPart = NT * kPartPitch * 4;
@@ -143,7 +147,9 @@ __device__ __forceinline__ uint32_t nv4_factor(uint32_t b) {
   return h;
 }
 
-template <int FMT, int NT, int SRC>
+// WHOLE: k is a multiple of 256, so that every row's scale bytes start aligned
+// and no stage is cut short.
+template <int FMT, int NT, int SRC, bool WHOLE>
 __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
                                   NT == 64 ? 1 : 2)
     rows_f4_kernel(const RowArgs a) {
@@ -154,6 +160,7 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
   __shared__ int s_rows[kSegment];
   __shared__ int s_count[kSegment / 32 + 1];
   __shared__ float s_fac[2][NT];
+  __shared__ uint32_t s_max[2][NT * P::kUnits / 32];
   __shared__ int s_exp[NT];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -177,45 +184,53 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
   const uint8_t *codes =
       a.codes + (expert * a.n + first) * code_pitch + (lane & 7) * 16;
   const uint8_t *scales = a.scales + (expert * a.n + first) * blocks;
-  const bool whole = a.k % kStageK == 0;
-  int64_t off[4];  // of the four rows this lane copies
+  uint32_t off[4];  // of the four rows this lane copies (k < 2^27)
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    off[i] = min((lane >> 3) + 4 * i, last) * code_pitch;
+    off[i] = (uint32_t)(min((lane >> 3) + 4 * i, last) * code_pitch);
+  // chunks t and t + 4 of row g in a stage (the odd rows' halves are swapped)
+  const uint32_t my_chunk =
+      g * (kStageK / 2) + ((t ^ ((g & 1) << 2)) << 4);
+  const uint32_t ring_at =
+      ring + (lane >> 3) * (kStageK / 2) +
+      (((lane & 7) ^ (((lane >> 3) & 1) << 2)) << 4);
 
   pdl_launch_dependents();
-  if ((lane & 7) == 0 && count > 0) {
-#pragma unroll
-    for (int p = 0; p < kRing - 1; ++p)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (p < count)
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(
-              codes + off[i] + (int64_t)(st0 + p) * (kStageK / 2)));
+  // Hint the L2 cache with this warp's codes, so that they are on their way
+  // while the kernel before finishes: lane r takes row r of the slice.
+  if (lane <= last && count > 0) {
+    const int64_t from = (int64_t)st0 * (kStageK / 2);
+    const int64_t to = (int64_t)st1 * (kStageK / 2);
+    const int64_t bytes = (to < code_pitch ? to : code_pitch) - from;
+    prefetch_l2_bulk(a.codes + (expert * a.n + first + lane) * code_pitch + from,
+                     (uint32_t)(bytes < kPrefetch ? bytes : kPrefetch));
   }
   pdl_wait();
 
-  auto issue = [&](int st) {  // stage st of the slice into the ring
+  // WHOLE: lanes 0 .. 15 copy a row's scale bytes each
+  const uint8_t *my_scales =
+      scales + min(lane, last) * blocks + (int64_t)st0 * P::kScaleRow;
+  codes += (int64_t)st0 * (kStageK / 2);
+  auto issue = [&](int st, int slot) {  // stage st of the slice into the ring
     if (st < count) {
-      const uint32_t dst = ring + (st % kRing) * P::kStage;
-      const int64_t at = (int64_t)(st0 + st) * (kStageK / 2);
-      const bool live = at + (lane & 7) * 16 < code_pitch;
+      const uint8_t *src = codes + st * (kStageK / 2);
+      const uint32_t dst = ring_at + slot * P::kStage;
+      const bool live =
+          WHOLE || (int64_t)(st0 + st) * (kStageK / 2) + (lane & 7) * 16 <
+                       code_pitch;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = (lane >> 3) + 4 * i;
-        cp_async<16>(dst + r * (kStageK / 2) +
-                         (((lane & 7) ^ ((r & 1) << 2)) << 4),
-                     live ? codes + off[i] + at : codes, live);
-      }
-      const uint32_t sdst = dst + P::kCodes;
-      const int64_t sat = (int64_t)(st0 + st) * P::kScaleRow;
-      if (whole) {
+      for (int i = 0; i < 4; ++i)
+        cp_async<16>(dst + 4 * i * (kStageK / 2), live ? src + off[i] : a.codes,
+                     live);
+      const uint32_t sdst = ring + slot * P::kStage + P::kCodes;
+      if constexpr (WHOLE) {
         if (lane < 16)
           cp_async<P::kScaleRow>(sdst + lane * P::kScalePitch,
-                                 scales + min(lane, last) * blocks + sat, true);
+                                 my_scales + st * P::kScaleRow, true);
       } else {
         // the aligned words around a row's bytes; a word that holds none of
         // them is not read
+        const int64_t sat = (int64_t)(st0 + st) * P::kScaleRow;
         constexpr int kW = P::kScaleRow / 4 + 1;
 #pragma unroll
         for (int j = 0; j < (16 * kW + 31) / 32; ++j) {
@@ -243,210 +258,249 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
     for (int i = 0; i < kTiles; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
-    int R0 = 0, R1 = 0;  // MX4: R of rows g and g + 8
-    int ex[P::kPerWarp];  // X (bf16) or R (MX4 x) of the rows this warp stages
+    uint32_t R = 0;  // MX4: R of row g in the low half, of row g + 8 above
+    // X (bf16) or R (MX4 x) of the rows of this thread's units
+    int ex[P::kPer];
 #pragma unroll
-    for (int i = 0; i < P::kPerWarp; ++i) ex[i] = SRC == kBf16 ? -112 : 0;
+    for (int j = 0; j < P::kPer; ++j) ex[j] = SRC == kBf16 ? -112 : 0;
 
 #pragma unroll 1
-    for (int p = 0; p < kRing - 1; ++p) issue(p);
+    for (int p = 0; p < kRing - 1; ++p) issue(p, p);
 
-    constexpr int kRegs = P::kPerWarp * P::kUnits;
-    XRegs<SRC, kRegs> xr;
-    auto load_x = [&](int st) {  // the buffer that starts with stage st
-      const int64_t k0 = (int64_t)(st0 + st) * kStageK;
-      const int64_t k_end =
-          (int64_t)st1 * kStageK < a.k ? (int64_t)st1 * kStageK : a.k;
+    // Rows of x, kXK values of each per buffer. Thread tid holds units
+    // tid + kThreads j, a warp's 32 units of one j lie in one row.
+    const int64_t k_end =
+        (int64_t)st1 * kStageK < a.k ? (int64_t)st1 * kStageK : a.k;
+    const int buffers = (count + P::kXStages - 1) / P::kXStages;
+    XRegs<SRC, P::kPer> xr;
+    auto load_x = [&](int i) {
+      if (i >= buffers) return;
+      const int64_t k0 = (int64_t)st0 * kStageK + (int64_t)i * P::kXK;
 #pragma unroll
-      for (int i = 0; i < P::kPerWarp; ++i) {
-        const int r = warp * P::kPerWarp + i;
+      for (int j = 0; j < P::kPer; ++j) {
+        const int q = tid + kThreads * j, r = q / P::kUnits;
+        const int64_t k = k0 + 8 * (q % P::kUnits);
+        const bool live = r < rows && k < k_end;
         const int64_t row =
-            r < rows ? (a.ids != nullptr ? s_rows[base + r] : b0 + r) : 0;
-#pragma unroll
-        for (int u = 0; u < P::kUnits; ++u) {
-          const int64_t k = k0 + 8 * (lane + 32 * u);
-          const bool live = r < rows && k < k_end;
-          const int j = i * P::kUnits + u;
-          if constexpr (SRC == kBf16) {
-            xr.v[j] = make_uint4(0, 0, 0, 0);
-            if (live)
-              xr.v[j] = __ldg(reinterpret_cast<const uint4 *>(a.x + row * a.ldx +
-                                                              k));
-          } else {
-            xr.v[j] = 0;
-            xr.s[j] = 0;
-            if (live) {
-              xr.v[j] = __ldg(reinterpret_cast<const uint32_t *>(
-                  a.xcodes + row * code_pitch + k / 2));
-              xr.s[j] = __ldg(a.xscales + row * blocks + k / f4_block(FMT));
-            }
+            !live ? 0 : a.ids != nullptr ? s_rows[base + r] : b0 + r;
+        if constexpr (SRC == kBf16) {
+          xr.v[j] = make_uint4(0, 0, 0, 0);
+          if (live)
+            xr.v[j] =
+                __ldg(reinterpret_cast<const uint4 *>(a.x + row * a.ldx + k));
+        } else {
+          xr.v[j] = 0;
+          xr.s[j] = 0;
+          if (live) {
+            xr.v[j] = __ldg(reinterpret_cast<const uint32_t *>(
+                a.xcodes + row * code_pitch + k / 2));
+            xr.s[j] = __ldg(a.xscales + row * blocks + k / f4_block(FMT));
           }
         }
       }
     };
-    // registers -> fp16 in buffer `buf`; whether a row's exponent rose
-    auto stage_x = [&](int buf) {
-      bool rose = false;
+    // The largest magnitude (bf16 bits) or scale byte of each warp's units.
+    constexpr bool kHasExp = SRC == kBf16 || FMT == TQ_FMT_MX4;
+    auto publish = [&](int i) {
+      if (!kHasExp || i >= buffers) return;
 #pragma unroll
-      for (int i = 0; i < P::kPerWarp; ++i) {
-        const int r = warp * P::kPerWarp + i;
-        float s = 0.0f;
+      for (int j = 0; j < P::kPer; ++j) {
+        if ((warp * 32 + kThreads * j) / P::kUnits >= rows) break;
+        uint32_t m;
         if constexpr (SRC == kBf16) {
+          m = __reduce_max_sync(0xFFFFFFFFu, max_mag8(xr.v[j]));
+          if (m >= 0x7F80u)  // NaN or Inf: take the largest finite value
+            m = __reduce_max_sync(0xFFFFFFFFu, max_finite8(xr.v[j]));
+        } else {
+          const uint32_t b = xr.s[j];
+          m = __reduce_max_sync(0xFFFFFFFFu, b == 255u ? 0u : b);
+        }
+        if (lane == 0) s_max[i & 1][warp + kWarps * j] = m;
+      }
+    };
+    // registers -> fp16 in buffer i & 1; whether a row's exponent rose
+    auto convert = [&](int i) {
+      bool rose = false;
+      if (i >= buffers) return rose;
+#pragma unroll
+      for (int j = 0; j < P::kPer; ++j) {
+        const int q = tid + kThreads * j, r = q / P::kUnits;
+        if ((warp * 32 + kThreads * j) / P::kUnits >= rows) break;
+        const int unit = q % P::kUnits;
+        if (kHasExp) {
           uint32_t m = 0;
 #pragma unroll
-          for (int u = 0; u < P::kUnits; ++u)
-            m = max(m, max_mag8(xr.v[i * P::kUnits + u]));
-          m = __reduce_max_sync(0xFFFFFFFFu, m);
-          if (m >= 0x7F80u) {  // NaN or Inf: take the largest finite value
-            m = 0;
-#pragma unroll
-            for (int u = 0; u < P::kUnits; ++u)
-              m = max(m, max_finite8(xr.v[i * P::kUnits + u]));
-            m = __reduce_max_sync(0xFFFFFFFFu, m);
-          }
-          const int e = (int)(m >> 7) - 127;
-          const int now = max(ex[i], e);
-          if (lane == 0) s_fac[buf][r] = pow2_down(ex[i] - now);
-          rose |= now != ex[i];
-          ex[i] = now;
-          // 2^(14 - X), X >= -112
-          s = __uint_as_float((uint32_t)(141 - now) << 23);
-        } else if (FMT == TQ_FMT_MX4) {
-          uint32_t m = 0;
-#pragma unroll
-          for (int u = 0; u < P::kUnits; ++u) {
-            const uint32_t b = xr.s[i * P::kUnits + u];
-            m = max(m, b == 255u ? 0u : b);
-          }
+          for (int u = 0; u < P::kUnits / 32; ++u)
+            m = max(m, s_max[i & 1][r * (P::kUnits / 32) + u]);
           const int now =
-              max(ex[i], (int)__reduce_max_sync(0xFFFFFFFFu, m));
-          if (lane == 0) s_fac[buf][r] = pow2_down(ex[i] - now);
-          rose |= now != ex[i];
-          ex[i] = now;
+              max(ex[j], SRC == kBf16 ? (int)(m >> 7) - 127 : (int)m);
+          if (unit == 0) s_fac[i & 1][r] = pow2_down(ex[j] - now);
+          rose |= now != ex[j];
+          ex[j] = now;
         }
-#pragma unroll
-        for (int u = 0; u < P::kUnits; ++u) {
-          const int j = i * P::kUnits + u;
-          const int unit = lane + 32 * u;  // of 8 k
-          uint4 h;
-          if constexpr (SRC == kBf16) {
-            h.x = scaled_h2(xr.v[j].x, s);
-            h.y = scaled_h2(xr.v[j].y, s);
-            h.z = scaled_h2(xr.v[j].z, s);
-            h.w = scaled_h2(xr.v[j].w, s);
-          } else {
-            uint32_t q[4];
-            f4x8_to_h2(xr.v[j], q);
-            const uint32_t f = FMT == TQ_FMT_MX4
-                                   ? mx4_factor((int)xr.s[j], ex[i])
-                                   : nv4_factor(xr.s[j]);
-            h = make_uint4(hmul2(q[0], f), hmul2(q[1], f), hmul2(q[2], f),
-                           hmul2(q[3], f));
-          }
-          // unit 4 t + s of a group of 128 k lies at position 4 s + t, so
-          // that the four lanes of a quad read 64 consecutive bytes
-          const int pos = (unit & ~15) | ((unit & 3) << 2) | ((unit >> 2) & 3);
-          sts128(xbuf + buf * P::kXBuf + r * P::kXPitch + pos * 16, h);
+        uint4 h;
+        if constexpr (SRC == kBf16) {
+          // 2^(14 - X), X >= -112
+          const float f = __uint_as_float((uint32_t)(141 - ex[j]) << 23);
+          h.x = scaled_h2(xr.v[j].x, f);
+          h.y = scaled_h2(xr.v[j].y, f);
+          h.z = scaled_h2(xr.v[j].z, f);
+          h.w = scaled_h2(xr.v[j].w, f);
+        } else {
+          uint32_t c[4];
+          f4x8_to_h2(xr.v[j], c);
+          const uint32_t f = FMT == TQ_FMT_MX4 ? mx4_factor((int)xr.s[j], ex[j])
+                                               : nv4_factor(xr.s[j]);
+          h = make_uint4(hmul2(c[0], f), hmul2(c[1], f), hmul2(c[2], f),
+                         hmul2(c[3], f));
         }
+        // unit 4 t + s of a group of 128 k lies at position 4 s + t, so that
+        // the four lanes of a quad read 64 consecutive bytes
+        const int pos = (unit & ~15) | ((unit & 3) << 2) | ((unit >> 2) & 3);
+        sts128(xbuf + (i & 1) * P::kXBuf + r * P::kXPitch + pos * 16, h);
       }
       return rose;
     };
 
     load_x(0);
-    int buf = 0;
+    for (int i = tid; i < 2 * (NT - rows) * (P::kXPitch / 16); i += kThreads) {
+      const int b = i / ((NT - rows) * (P::kXPitch / 16));
+      sts128(xbuf + b * P::kXBuf + rows * P::kXPitch +
+                 (i - b * (NT - rows) * (P::kXPitch / 16)) * 16,
+             make_uint4(0, 0, 0, 0));  // rows that are not there
+    }
+    publish(0);
+    __syncthreads();
+    int any = convert(0);
+    load_x(1);
+    publish(1);
+    any = __syncthreads_or(any);
+    int st = 0, slot = 0;
 #pragma unroll 1
-    for (int st = 0; st < count; buf ^= 1) {
-      const bool rose = stage_x(buf);
-      const int any = __syncthreads_or(rose);
-      const int end = st + P::kXStages < count ? st + P::kXStages : count;
-      if (end < count) load_x(end);
+    for (int i = 0; i < buffers; ++i) {
+      const int rose = convert(i + 1);
+      load_x(i + 2);
       if (any) {
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i) {
-          const float f0 = s_fac[buf][8 * i + 2 * t];
-          const float f1 = s_fac[buf][8 * i + 2 * t + 1];
-          acc[i][0] *= f0;
-          acc[i][1] *= f1;
-          acc[i][2] *= f0;
-          acc[i][3] *= f1;
+        for (int c = 0; c < kTiles; ++c) {
+          const float f0 = s_fac[i & 1][8 * c + 2 * t];
+          const float f1 = s_fac[i & 1][8 * c + 2 * t + 1];
+          acc[c][0] *= f0;
+          acc[c][1] *= f1;
+          acc[c][2] *= f0;
+          acc[c][3] *= f1;
         }
       }
-      uint32_t xat = xbuf + buf * P::kXBuf + g * P::kXPitch + t * 16;
+      const int end = st + P::kXStages < count ? st + P::kXStages : count;
+      uint32_t xat = xbuf + (i & 1) * P::kXBuf + g * P::kXPitch + t * 16;
 #pragma unroll 1
       for (; st < end; ++st, xat += 2 * kStageK) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
         __syncwarp();
-        issue(st + kRing - 1);
-        const uint32_t src = ring + (st % kRing) * P::kStage;
-        // scale bytes of chunks t and t + 4 of rows g and g + 8
+        issue(st + kRing - 1, slot == 0 ? kRing - 1 : slot - 1);
+        const uint32_t src = ring + slot * P::kStage;
+        slot = slot == kRing - 1 ? 0 : slot + 1;
+        // fp16 factors of chunks t and t + 4 of rows g and g + 8
         uint32_t f[2][2][2];  // [half][row][block of the chunk]
-        {
-          constexpr int kB = FMT == TQ_FMT_MX4 ? 1 : 2;
-          uint32_t b[2][2][kB];
-          const uint32_t s0 = src + P::kCodes;
+        const uint32_t s0 = src + P::kCodes + g * P::kScalePitch;
+        // rows that do not start on a word boundary lie shifted, and bytes
+        // past the row's end belong to the next row
+        auto odd_byte = [&](int r, int j) {
+          const uint32_t shift =
+              (uint32_t)(reinterpret_cast<uintptr_t>(
+                             scales + min(g + 8 * r, last) * blocks) &
+                         3u);
+          const uint32_t b = lds_u8(s0 + 8 * r * P::kScalePitch + shift + j);
+          return (int64_t)(st0 + st) * P::kScaleRow + j < blocks ? b : 0u;
+        };
+        if constexpr (FMT == TQ_FMT_MX4) {
+          uint32_t e[2];  // [row]: chunk t in the low half, t + 4 above
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const int row = g + 8 * r;
-            // rows that do not start on a word boundary lie shifted
-            const uint32_t shift =
-                whole ? 0u
-                      : (uint32_t)(reinterpret_cast<uintptr_t>(
-                                       scales + min(row, last) * blocks) &
-                                   3u);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int c = 0; c < kB; ++c) {
-                const int j = (t + 4 * h) * kB + c;
-                b[h][r][c] = lds_u8(s0 + row * P::kScalePitch + shift + j);
-                if (!whole && (int64_t)(st0 + st) * P::kScaleRow + j >= blocks)
-                  b[h][r][c] = 0;  // past the row's end
-              }
-          }
-          if constexpr (FMT == TQ_FMT_MX4) {
-            uint32_t m = 0;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t e0 = b[h][0][0] == 255u ? 0u : b[h][0][0];
-              const uint32_t e1 = b[h][1][0] == 255u ? 0u : b[h][1][0];
-              m = __vmaxu2(m, e0 | e1 << 16);
+            if constexpr (WHOLE) {
+              uint32_t lo, hi;
+              asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];"
+                           : "=r"(lo), "=r"(hi)
+                           : "r"(s0 + 8 * r * P::kScalePitch)
+                           : "memory");
+              e[r] = __byte_perm(lo, hi, t | (t + 4) << 8) & 0x00FF00FFu;
+            } else {
+              e[r] = odd_byte(r, t) | odd_byte(r, t + 4) << 16;
             }
+          }
+          // largest of each row over the quad, row g low, row g + 8 high
+          auto quad_max = [&](uint32_t e0, uint32_t e1) {
+            uint32_t m = __vmaxu2(__byte_perm(e0, e1, 0x5410),
+                                  __byte_perm(e0, e1, 0x7632));
             m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-            m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-            const int n0 = max(R0, (int)(m & 0xFFFFu));
-            const int n1 = max(R1, (int)(m >> 16));
-            if (__any_sync(0xFFFFFFFFu, n0 != R0 || n1 != R1)) {
-              const float f0 = pow2_down(R0 - n0), f1 = pow2_down(R1 - n1);
-#pragma unroll
-              for (int i = 0; i < kTiles; ++i) {
-                acc[i][0] *= f0;
-                acc[i][1] *= f0;
-                acc[i][2] *= f1;
-                acc[i][3] *= f1;
-              }
-              R0 = n0;
-              R1 = n1;
+            return __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+          };
+          uint32_t now = __vmaxu2(R, quad_max(e[0], e[1]));
+          bool nan = false;
+          if (__any_sync(0xFFFFFFFFu, now != R)) {
+            nan = __any_sync(0xFFFFFFFFu, (now & 0xFFFFu) == 255u ||
+                                              now >> 16 == 255u);
+            if (nan) {  // NaN scales do not count
+              auto drop = [](uint32_t v) {
+                return ((v & 0xFFFFu) == 255u ? 0u : v & 0xFFFFu) |
+                       (v >> 16 == 255u ? 0u : v & 0xFFFF0000u);
+              };
+              now = __vmaxu2(R, quad_max(drop(e[0]), drop(e[1])));
             }
+            const float f0 =
+                pow2_down((int)(R & 0xFFFFu) - (int)(now & 0xFFFFu));
+            const float f1 = pow2_down((int)(R >> 16) - (int)(now >> 16));
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              f[h][0][0] = f[h][0][1] = mx4_factor((int)b[h][0][0], R0);
-              f[h][1][0] = f[h][1][1] = mx4_factor((int)b[h][1][0], R1);
+            for (int c = 0; c < kTiles; ++c) {
+              acc[c][0] *= f0;
+              acc[c][1] *= f0;
+              acc[c][2] *= f1;
+              acc[c][3] *= f1;
             }
-          } else {
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int r = 0; r < 2; ++r) {
-                f[h][r][0] = nv4_factor(b[h][r][0]);
-                f[h][r][1] = nv4_factor(b[h][r][kB - 1]);
-              }
+            R = now;
           }
-        }
 #pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            // exponent fields E - R + 28 of both chunks, at least 0: kept
+            // 256 too large while they may be negative
+            const uint32_t d = (r == 0 ? R & 0xFFFFu : R >> 16) * 0x00010001u;
+            const uint32_t v =
+                __vmaxu2(e[r] + 0x011C011Cu - d, 0x01000100u) & 0x00FF00FFu;
+            f[0][r][0] = f[0][r][1] = __byte_perm(v, 0, 0x1010) << 10;
+            f[1][r][0] = f[1][r][1] = __byte_perm(v, 0, 0x3232) << 10;
+            if (nan) {
+              if ((e[r] & 0xFFFFu) == 255u)
+                f[0][r][0] = f[0][r][1] = 0x7E007E00u;
+              if (e[r] >> 16 == 255u) f[1][r][0] = f[1][r][1] = 0x7E007E00u;
+            }
+          }
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              uint32_t b, v;
+              if constexpr (WHOLE)
+                asm volatile("ld.shared.u16 %0, [%1];"
+                             : "=r"(b)
+                             : "r"(s0 + 8 * r * P::kScalePitch + 2 * t + 8 * h)
+                             : "memory");
+              else
+                b = odd_byte(r, 2 * t + 8 * h) |
+                    odd_byte(r, 2 * t + 8 * h + 1) << 8;
+              asm("cvt.rn.f16x2.e4m3x2 %0, %1;"
+                  : "=r"(v)
+                  : "h"((uint16_t)(b & 0x7F7Fu)));
+              f[h][r][0] = __byte_perm(v, 0, 0x1010);
+              f[h][r][1] = __byte_perm(v, 0, 0x3232);
+            }
+        }
+        // not unrolled: the two halves together overran the instruction cache
+#pragma unroll 1
         for (int h = 0; h < 2; ++h) {
-          const uint32_t chunk = (uint32_t)(t + 4 * h) ^ ((g & 1) << 2);
-          const uint4 c0 = lds128(src + g * (kStageK / 2) + chunk * 16);
-          const uint4 c1 = lds128(src + (g + 8) * (kStageK / 2) + chunk * 16);
+          const uint32_t at = src + (h == 0 ? my_chunk : my_chunk ^ 64u);
+          const uint4 c0 = lds128(at);
+          const uint4 c1 = lds128(at + 8 * (kStageK / 2));
           const uint32_t w0[4] = {c0.x, c0.y, c0.z, c0.w};
           const uint32_t w1[4] = {c1.x, c1.y, c1.z, c1.w};
 #pragma unroll
@@ -455,26 +509,32 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
             f4x8_to_h2(w0[s], p);
             f4x8_to_h2(w1[s], q);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              p[i] = hmul2(p[i], f[h][0][s >> 1]);
-              q[i] = hmul2(q[i], f[h][1][s >> 1]);
+            for (int c = 0; c < 4; ++c) {
+              p[c] = hmul2(p[c], f[0][0][s >> 1]);
+              q[c] = hmul2(q[c], f[0][1][s >> 1]);
             }
 #pragma unroll
-            for (int i = 0; i < kTiles; ++i) {
+            for (int c = 0; c < kTiles; ++c) {
               const uint4 v =
-                  lds128(xat + 256 * h + 8 * i * P::kXPitch + 64 * s);
-              mma_f16(acc[i], p[0], q[0], p[1], q[1], v.x, v.y);
-              mma_f16(acc[i], p[2], q[2], p[3], q[3], v.z, v.w);
+                  lds128(xat + 256 * h + 8 * c * P::kXPitch + 64 * s);
+              mma_f16(acc[c], p[0], q[0], p[1], q[1], v.x, v.y);
+              mma_f16(acc[c], p[2], q[2], p[3], q[3], v.z, v.w);
             }
           }
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) f[0][r][c] = f[1][r][c];
         }
       }
+      publish(i + 2);
+      any = __syncthreads_or(rose);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    if (lane == 0) {
 #pragma unroll
-      for (int i = 0; i < P::kPerWarp; ++i)
-        s_exp[warp * P::kPerWarp + i] = ex[i];
+    for (int j = 0; j < P::kPer; ++j) {
+      const int q = tid + kThreads * j;
+      if (q % P::kUnits == 0) s_exp[q / P::kUnits] = ex[j];
     }
     __syncthreads();  // rings are free, exponents are there
 
@@ -486,7 +546,7 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
       for (int j = 0; j < 4; ++j) {
         const int b = 8 * i + 2 * t + (j & 1);
         int e = 0;
-        if (FMT == TQ_FMT_MX4) e += (j < 2 ? R0 : R1) - 140;
+        if (FMT == TQ_FMT_MX4) e += (int)(j < 2 ? R & 0xFFFFu : R >> 16) - 140;
         if (SRC == kBf16)
           e += s_exp[b] - 14;
         else if (FMT == TQ_FMT_MX4)
@@ -607,13 +667,64 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
   }
 }
 
-template <int FMT, int NT, int SRC>
-cudaError_t launch(const RowArgs &a, int64_t grid_y, cudaStream_t stream) {
+// Clusters of ks CTAs that are resident together, asked once per kernel, ks
+// and device.
+template <int FMT, int NT, int SRC, bool WHOLE>
+int resident(int ks, int dev) {
+  static std::atomic<int> known[16][9];  // 0: not asked yet
   using P = RowPlan<FMT, NT>;
-  auto kern = rows_f4_kernel<FMT, NT, SRC>;
-  cudaError_t e = ensure_smem_limit<rows_f4_kernel<FMT, NT, SRC>>(P::kSmem);
+  if (dev < 16) {
+    const int v = known[dev][ks].load(std::memory_order_relaxed);
+    if (v != 0) return v;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ks);
+  cfg.blockDim = dim3(P::kThreads);
+  cfg.dynamicSmemBytes = P::kSmem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ks;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(
+          &n, reinterpret_cast<const void *>(
+              rows_f4_kernel<FMT, NT, SRC, WHOLE>),
+          &cfg) != cudaSuccess ||
+      n < 1) {
+    cudaGetLastError();
+    n = 1;
+  }
+  if (dev < 16) known[dev][ks].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// `copies`: how many row products of n rows run at once (passes, experts).
+template <int FMT, int NT, int SRC, bool WHOLE>
+cudaError_t launch_whole(RowArgs a, int64_t copies, int64_t grid_y,
+                   cudaStream_t stream) {
+  using P = RowPlan<FMT, NT>;
+  auto kern = rows_f4_kernel<FMT, NT, SRC, WHOLE>;
+  cudaError_t e =
+      ensure_smem_limit<rows_f4_kernel<FMT, NT, SRC, WHOLE>>(P::kSmem);
   if (e != cudaSuccess) return e;
+  int dev = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   const int64_t tiles = (a.n + P::kTile - 1) / P::kTile;
+  const int64_t stages = (a.k + kStageK - 1) / kStageK;
+  // The widest split of K whose clusters are all resident at once, with two
+  // stages at least per CTA: a second wave costs a whole pass of start-up and
+  // reduction (8192 x 5376, batch 1: 17.5 us with 320 CTAs on 296 places).
+  a.ks = 1;
+  for (int ks = 8; ks > 1; --ks)
+    if (2 * ks <= stages &&
+        tiles * copies <= resident<FMT, NT, SRC, WHOLE>(ks, dev)) {
+      a.ks = ks;
+      break;
+    }
+  if (g_force_ks > 0) a.ks = g_force_ks;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * a.ks), (unsigned)grid_y);
   cfg.blockDim = dim3(P::kThreads);
@@ -631,49 +742,39 @@ cudaError_t launch(const RowArgs &a, int64_t grid_y, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
+template <int FMT, int NT, int SRC>
+cudaError_t launch(const RowArgs &a, int64_t copies, int64_t grid_y,
+                   cudaStream_t stream) {
+  return a.k % kStageK == 0
+             ? launch_whole<FMT, NT, SRC, true>(a, copies, grid_y, stream)
+             : launch_whole<FMT, NT, SRC, false>(a, copies, grid_y, stream);
+}
+
 template <int SRC>
-cudaError_t launch_nt(int format, int nt, const RowArgs &a, int64_t grid_y,
-                      cudaStream_t stream) {
+cudaError_t launch_nt(int format, int nt, const RowArgs &a, int64_t copies,
+                      int64_t grid_y, cudaStream_t stream) {
   const bool mx = format == TQ_FMT_MX4;
   switch (nt) {
     case 8:
-      return mx ? launch<TQ_FMT_MX4, 8, SRC>(a, grid_y, stream)
-                : launch<TQ_FMT_NV4, 8, SRC>(a, grid_y, stream);
+      return mx ? launch<TQ_FMT_MX4, 8, SRC>(a, copies, grid_y, stream)
+                : launch<TQ_FMT_NV4, 8, SRC>(a, copies, grid_y, stream);
     case 16:
-      return mx ? launch<TQ_FMT_MX4, 16, SRC>(a, grid_y, stream)
-                : launch<TQ_FMT_NV4, 16, SRC>(a, grid_y, stream);
+      return mx ? launch<TQ_FMT_MX4, 16, SRC>(a, copies, grid_y, stream)
+                : launch<TQ_FMT_NV4, 16, SRC>(a, copies, grid_y, stream);
     default: break;
   }
   if constexpr (SRC == kBf16) {
     if (nt == 32)
-      return mx ? launch<TQ_FMT_MX4, 32, SRC>(a, grid_y, stream)
-                : launch<TQ_FMT_NV4, 32, SRC>(a, grid_y, stream);
-    return mx ? launch<TQ_FMT_MX4, 64, SRC>(a, grid_y, stream)
-              : launch<TQ_FMT_NV4, 64, SRC>(a, grid_y, stream);
+      return mx ? launch<TQ_FMT_MX4, 32, SRC>(a, copies, grid_y, stream)
+                : launch<TQ_FMT_NV4, 32, SRC>(a, copies, grid_y, stream);
+    return mx ? launch<TQ_FMT_MX4, 64, SRC>(a, copies, grid_y, stream)
+              : launch<TQ_FMT_NV4, 64, SRC>(a, copies, grid_y, stream);
   }
   return cudaErrorInvalidValue;
 }
 
 int rows_per_pass(int64_t rows) {
   return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-}
-
-// CTAs of a cluster: enough for every place on the device, at least two
-// stages of K each.
-cudaError_t split(int64_t n, int64_t k, int nt, int64_t copies, int *ks) {
-  int dev = 0, sms = 148;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const int64_t stages = (k + kStageK - 1) / kStageK;
-  const int64_t tile = nt == 64 ? 256 : 128, places = nt == 64 ? sms : 2 * sms;
-  const int64_t tiles = (n + tile - 1) / tile * copies;
-  int64_t c = (places + tiles - 1) / tiles;
-  if (c > stages / 2) c = stages / 2;
-  if (c > 8) c = 8;
-  if (c < 1) c = 1;
-  *ks = (int)c;
-  return cudaSuccess;
 }
 
 RowArgs weight_args(const WeightsView &w) {
@@ -699,7 +800,7 @@ cudaError_t linear_f4_bf16(const WeightsView &w, const __nv_bfloat16 *x,
   a.ldy = ldy;
   const int nt = rows_per_pass(batch);
   const int64_t passes = (batch + nt - 1) / nt;
-  cudaError_t e = split(w.n, w.k, nt, passes, &a.ks);
+  cudaError_t e = cudaSuccess;
   // a grid's second dimension ends at 65535
   for (int64_t p = 0; p < passes && e == cudaSuccess; p += 65535) {
     const int64_t now = passes - p < 65535 ? passes - p : 65535;
@@ -707,7 +808,7 @@ cudaError_t linear_f4_bf16(const WeightsView &w, const __nv_bfloat16 *x,
     b.x += p * nt * ldx;
     b.y = y + p * nt * ldy;
     b.batch -= p * nt;
-    e = launch_nt<kBf16>(w.format, nt, b, now, stream);
+    e = launch_nt<kBf16>(w.format, nt, b, now, now, stream);
   }
   return e;
 }
@@ -729,9 +830,7 @@ cudaError_t launch_linear_experts_f4(const WeightsView &w, int n_experts,
   // experts that get rows at all, and the rows of one
   const int64_t used = tokens < n_experts ? tokens : n_experts;
   const int nt = rows_per_pass(2 * ((tokens + n_experts - 1) / n_experts));
-  const cudaError_t e = split(w.n, w.k, nt, used, &a.ks);
-  if (e != cudaSuccess) return e;
-  return launch_nt<kBf16>(w.format, nt, a, n_experts, stream);
+  return launch_nt<kBf16>(w.format, nt, a, used, n_experts, stream);
 }
 
 bool rows_f4_packed_supported(const WeightsView &x) { return x.n <= 16; }
@@ -746,10 +845,7 @@ cudaError_t rows_f4_packed(const WeightsView &w, const WeightsView &x, void *y,
   a.y = y;
   a.ldy = ldy;
   a.y_bf16 = y_type == TQ_Y_BF16;
-  const int nt = rows_per_pass(x.n);
-  const cudaError_t e = split(w.n, w.k, nt, 1, &a.ks);
-  if (e != cudaSuccess) return e;
-  return launch_nt<kPacked>(w.format, nt, a, 1, stream);
+  return launch_nt<kPacked>(w.format, rows_per_pass(x.n), a, 1, 1, stream);
 }
 
 }  // namespace tq

@@ -11,10 +11,12 @@
 //
 // Every decision equals exact arithmetic. MX4: v 2^-E is exact in fp32. NV4:
 // quotients are taken as products with a reciprocal (relative error below
-// 2^-21), and where one lies within 2^-19 of a border between two results
-// the block is decided again in fp64: s g has 28 significant bits and a
-// border times it at most 31, v has 8, so v and a border that differ do so
-// by more than 2^-40 relative, far above the 2^-53 of an fp64 quotient.
+// 2^-21), and one within 2^-19 of a border t between two results is settled
+// by the sign of v - t d, d = s g (or 6 g): d as the unrounded sum of two fp32
+// numbers makes it exact in two fused multiply-adds. Such quotients are not
+// rare: with g = max|W| / 2688 and values of 8 significant bits, many lie at a
+// border but for the rounding of g (deciding them in fp64, a division each,
+// made the kernel 6 times slower than the MX4 one).
 #include "tq_f4.cuh"
 
 namespace tq {
@@ -27,6 +29,18 @@ __device__ __forceinline__ uint32_t max_mag8(const uint4 &w) {
   return max(m >> 16, m & 0xFFFFu);
 }
 
+// The same over the finite values, one by one.
+__device__ __noinline__ uint32_t max_finite8(uint4 w) {
+  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t a = (v[i >> 1] >> (16 * (i & 1))) & 0x7FFFu;
+    if (a < 0x7F80u) m = max(m, a);
+  }
+  return m;
+}
+
 __device__ __forceinline__ float bf16_lo(uint32_t w) {
   return __uint_as_float(w << 16);
 }
@@ -34,17 +48,7 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) {
   return __uint_as_float(w & 0xFFFF0000u);
 }
 
-// Two E2M1 codes (nearest even, at most 6): lo in bits 0-3, hi in bits 4-7.
-__device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
-  uint32_t r;
-  asm("{\n .reg .b8 t;\n cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n"
-      " mov.b32 %0, {t, 0, 0, 0};\n}"
-      : "=r"(r)
-      : "f"(hi), "f"(lo));
-  return r;
-}
-
-// The 8 codes of q[0..7].
+// The 8 E2M1 codes of q[0..7] (nearest even, at most 6), q[0] lowest.
 __device__ __forceinline__ uint32_t e2m1x8(const float (&q)[8]) {
   uint32_t r;
   asm("{\n .reg .b8 t0, t1, t2, t3;\n"
@@ -87,9 +91,41 @@ __device__ __forceinline__ float nv4_tensor_scale(float amax) {
   return amax == 0.0f ? 1.0f : (float)((double)amax / 2688.0);
 }
 
+// d = hi + lo exactly.
+struct Two {
+  float hi, lo;
+};
+
+__device__ __forceinline__ Two two_product(float a, float b) {
+  Two d;
+  d.hi = a * b;
+  d.lo = fmaf(a, b, -d.hi);
+  return d;
+}
+
+// A quotient q ~ v / d whose bits below the top BITS are within 16 of a
+// border's (all zero): the border itself where v / d is exactly on it, else
+// the number next to the border on the side of v / d.
+template <uint32_t BITS>
+__device__ __forceinline__ bool near_border(float q) {
+  return ((__float_as_uint(q) + 16u) & ((1u << BITS) - 1u)) < 32u;
+}
+
+template <uint32_t BITS>
+__device__ __forceinline__ float settle(float q, float v, const Two &d) {
+  const uint32_t u =
+      (__float_as_uint(q) + (1u << (BITS - 1))) & ~((1u << BITS) - 1u);
+  const float t = __uint_as_float(u);
+  if (t == 0.0f || fabsf(t) > 1e9f) return t;  // Inf among them: saturates
+  const float r = fmaf(-t, d.lo, fmaf(-t, d.hi, v));
+  if (r == 0.0f) return t;
+  return __uint_as_float((r > 0.0f) == (t > 0.0f) ? u + 1u : u - 1u);
+}
+
 // What an NV4 call derives from g once per thread.
 struct Nv4 {
   float g, inv_g, inv_6g;
+  Two six_g;
   bool exact;  // g so large or small that the fp32 quotients may be off
 };
 
@@ -98,18 +134,18 @@ __device__ __forceinline__ Nv4 nv4_make(float g) {
   s.g = g;
   s.inv_g = 1.0f / g;
   s.inv_6g = s.inv_g * (1.0f / 6.0f);
+  s.six_g = two_product(6.0f, g);
   s.exact = !(g > 1e-30f && g < 1e30f);
   return s;
 }
 
-// Block scale byte of an NV4 block with the largest magnitude `top`.
+// Block scale byte of an NV4 block with the largest magnitude `top`. Borders
+// lie halfway between E4M3 values: at most 5 significant bits, and below 2^-6
+// odd multiples of 2^-10, so their low 19 bits are clear.
 __device__ __forceinline__ uint32_t nv4_scale(float top, const Nv4 &s) {
-  const float r = top * s.inv_6g;
-  // Borders lie halfway between E4M3 values: at most 5 significant bits, and
-  // below 2^-6 odd multiples of 2^-10. Both have the low 19 bits clear.
-  const bool near = ((__float_as_uint(r) + 16u) & 0x7FFFFu) < 32u;
-  if ((near && r != 0.0f) || s.exact)
-    return e4m3_of_f64((double)top / (6.0 * (double)s.g));
+  if (s.exact) return e4m3_of_f64((double)top / (6.0 * (double)s.g));
+  float r = top * s.inv_6g;
+  if (near_border<19>(r)) r = settle<19>(r, top, s.six_g);
   uint16_t b;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
       : "=h"(b)
@@ -118,10 +154,10 @@ __device__ __forceinline__ uint32_t nv4_scale(float top, const Nv4 &s) {
 }
 
 template <int FMT>
-__device__ __forceinline__ void quantize8(const uint4 &w, bool live,
-                                          const Nv4 &s, uint32_t *codes,
-                                          uint32_t *byte, bool *bad) {
-  uint32_t m = live ? max_mag8(w) : 0u;
+__device__ __forceinline__ void quantize8(const uint4 &w, const Nv4 &s,
+                                          uint32_t *codes, uint32_t *byte,
+                                          bool *bad) {
+  uint32_t m = max_mag8(w);
   m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
   if (FMT == TQ_FMT_MX4) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
   if (m >= 0x7F80u) {  // NaN or Inf in the block
@@ -132,7 +168,7 @@ __device__ __forceinline__ void quantize8(const uint4 &w, bool live,
   }
   float inv, q[8];
   const float top = __uint_as_float(m << 16);
-  double d = 0.0;
+  float sf = 0.0f;
   if (FMT == TQ_FMT_MX4) {
     // bf16 exponent field f: floor(log2 top) = f - 127, so the byte is
     // f - 2; subnormal maxima (f = 0) clamp to 0 as well
@@ -141,153 +177,195 @@ __device__ __forceinline__ void quantize8(const uint4 &w, bool live,
     inv = __uint_as_float((254u - *byte) << 23);  // 2^(127 - byte)
   } else {
     *byte = nv4_scale(top, s);
-    const float sf = e4m3_to_f32(*byte);
+    sf = e4m3_to_f32(*byte);
     inv = sf == 0.0f ? 0.0f : __fdividef(s.inv_g, sf);
-    d = (double)sf * (double)s.g;
   }
   const uint32_t v[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    q[2 * i] = bf16_lo(v[i]) * inv;
-    q[2 * i + 1] = bf16_hi(v[i]) * inv;
+    asm("{\n .reg .b64 a, b;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %4};\n"
+        " mul.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, a;\n}"
+        : "=f"(q[2 * i]), "=f"(q[2 * i + 1])
+        : "f"(bf16_lo(v[i])), "f"(bf16_hi(v[i])), "f"(inv));
   }
-  *codes = e2m1x8(q);
   if (FMT == TQ_FMT_NV4) {
-    // Borders are odd multiples of 1/4, 1/2, 1 with at most 3 significant
-    // bits: the low 21 bits of q are clear there.
-    uint32_t close = 0xFFFFFFFFu;
+    // Borders of E2M1 have at most 3 significant bits: their low 21 bits are
+    // clear.
+    const Two d = two_product(sf, s.g);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const uint32_t u = max(__float_as_uint(q[i]) & 0x7FFFFFFFu, 0x3E010000u);
-      close = min(close, (u + 16u) & 0x1FFFFFu);
+      if (__builtin_expect(near_border<21>(q[i]), 0))
+        q[i] = settle<21>(q[i], i & 1 ? bf16_hi(v[i / 2]) : bf16_lo(v[i / 2]),
+                          d);
     }
-    if ((close < 32u || s.exact) && inv != 0.0f) {
-      uint32_t c = 0;
+  }
+  *codes = e2m1x8(q);
+  if (FMT == TQ_FMT_NV4 && s.exact && sf != 0.0f) {
+    const double d = (double)sf * (double)s.g;
+    uint32_t c = 0;
 #pragma unroll 1
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t h = v[0] * (i < 2) + v[1] * (i >> 1 == 1) +
-                           v[2] * (i >> 1 == 2) + v[3] * (i >> 1 == 3);
-        c |= e2m1_of_f64(i & 1 ? bf16_hi(h) : bf16_lo(h), d) << (4 * i);
-      }
-      *codes = c;
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t h = i < 2 ? v[0] : i < 4 ? v[1] : i < 6 ? v[2] : v[3];
+      c |= e2m1_of_f64(i & 1 ? bf16_hi(h) : bf16_lo(h), d) << (4 * i);
     }
+    *codes = c;
   }
 }
 
-// One lane per 8 values; `units` = n * k / 8. MODE 0: MX4; 1: NV4 with g in
-// *ts; 2: NV4 with max |W| in *ts.
-template <int FMT, bool AMAX>
+// `rows` rows of `units` 16-byte units (8 values), `pitch` units apart; a dense
+// matrix comes as one row. A block takes kPer * 256 consecutive units of a
+// row, a thread every 256th of them, so that kPer loads are in flight.
+constexpr int kPer = 4, kChunk = 256 * kPer;
+
+template <int FMT>
 __global__ void __launch_bounds__(256)
-    quantize_f4_kernel(const uint16_t *__restrict__ W, int64_t units,
-                       int64_t row_units, int64_t ldw,
+    quantize_f4_kernel(const uint4 *__restrict__ W, int64_t rows,
+                       int64_t units, int64_t pitch,
                        uint32_t *__restrict__ codes,
                        uint8_t *__restrict__ scales, const float *ts,
                        int32_t *status) {
+  pdl_launch_dependents();
+  pdl_wait();
   Nv4 s = {};
   bool bad = false, bad_g = false;
   if (FMT == TQ_FMT_NV4) {
-    const float g = AMAX ? nv4_tensor_scale(*ts) : *ts;
+    const float g = *ts;
     bad_g = !(g > 0.0f && g < __int_as_float(0x7F800000));
     s = nv4_make(bad_g ? 1.0f : g);
   }
-  const int64_t step = (int64_t)gridDim.x * blockDim.x;
-  const int64_t first = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  // whole warps run the shuffles: the loop count is the block's
-  const int64_t rounds =
-      (units - (int64_t)blockIdx.x * blockDim.x + step - 1) / step;
-  for (int64_t r = 0; r < rounds; ++r) {
-    const int64_t u = first + r * step;
-    const bool live = u < units;
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (live) {
-      const int64_t row = u / row_units;
-      w = __ldg(reinterpret_cast<const uint4 *>(W + row * ldw) +
-                (u - row * row_units));
+  for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
+    const uint4 *src = W + row * pitch;
+    for (int64_t u0 = (int64_t)blockIdx.x * kChunk + threadIdx.x;
+         u0 - threadIdx.x < units; u0 += (int64_t)gridDim.x * kChunk) {
+      uint4 w[kPer];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        w[i] = make_uint4(0, 0, 0, 0);
+        if (u0 + 256 * i < units) w[i] = __ldg(src + u0 + 256 * i);
+      }
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int64_t u = u0 + 256 * i;
+        uint32_t c, b;
+        quantize8<FMT>(w[i], s, &c, &b, &bad);
+        if (u >= units) continue;
+        if (bad_g) {
+          c = 0;
+          b = 0x7Fu;
+        }
+        constexpr int kLanes = f4_block(FMT) / 8;
+        const int64_t at = row * units + u;
+        codes[at] = c;
+        if (threadIdx.x % kLanes == 0) scales[at / kLanes] = (uint8_t)b;
+      }
     }
-    uint32_t c, b;
-    quantize8<FMT>(w, live, s, &c, &b, &bad);
-    if (!live) continue;
-    if (bad_g) {
-      c = 0;
-      b = 0x7Fu;
-    }
-    codes[u] = c;
-    constexpr int kLanes = FMT == TQ_FMT_MX4 ? 4 : 2;
-    if (u % kLanes == 0) scales[u / kLanes] = (uint8_t)b;
   }
   if (bad) report(status, TQ_ERR_NONFINITE);
   if (bad_g && threadIdx.x == 0) report(status, TQ_ERR_INVALID_ARG);
 }
 
-// max |W| over the finite values, as fp32 bits (magnitudes order like them).
+// max |W| over the finite values, as bf16 bits (magnitudes order like them),
+// in scratch[0]; the last block to arrive (scratch[1] counts them) turns it
+// into g. Goes from the end of the matrix to its front.
 __global__ void __launch_bounds__(256)
-    amax_f4_kernel(const uint16_t *__restrict__ W, int64_t units,
-                   int64_t row_units, int64_t ldw, uint32_t *out) {
+    amax_f4_kernel(const uint4 *__restrict__ W, int64_t rows, int64_t units,
+                   int64_t pitch, uint32_t *scratch, float *ts) {
+  pdl_launch_dependents();
+  pdl_wait();
   uint32_t m = 0;
-  for (int64_t u = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; u < units;
-       u += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t row = u / row_units;
-    const uint4 w = __ldg(reinterpret_cast<const uint4 *>(W + row * ldw) +
-                          (u - row * row_units));
-    const uint32_t t = max_mag8(w);
-    if (t < 0x7F80u) {
-      m = max(m, t);
-    } else {  // some value is not finite: take the others one by one
-      const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+  const int64_t chunks = (units + kChunk - 1) / kChunk;
+  for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
+    const uint4 *src = W + (rows - 1 - r) * pitch;
+    for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+      const int64_t u0 = (chunks - 1 - c) * kChunk + threadIdx.x;
+      uint4 w[kPer];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t a = (v[i >> 1] >> (16 * (i & 1))) & 0x7FFFu;
-        if (a < 0x7F80u) m = max(m, a);
+      for (int i = 0; i < kPer; ++i) {
+        w[i] = make_uint4(0, 0, 0, 0);
+        if (u0 + 256 * i < units) w[i] = __ldg(src + u0 + 256 * i);
+      }
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        uint32_t t = max_mag8(w[i]);
+        if (t >= 0x7F80u) t = max_finite8(w[i]);
+        m = max(m, t);
       }
     }
   }
   m = __reduce_max_sync(0xFFFFFFFFu, m);
-  if ((threadIdx.x & 31) == 0 && m != 0) atomicMax(out, m << 16);
+  __shared__ uint32_t s_m[8];
+  if ((threadIdx.x & 31) == 0) s_m[threadIdx.x >> 5] = m;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m = max(m, s_m[i]);
+  atomicMax(scratch, m);
+  __threadfence();
+  if (atomicAdd(scratch + 1, 1u) == gridDim.x * gridDim.y - 1) {
+    __threadfence();
+    const uint32_t all = atomicMax(scratch, 0u);
+    *ts = nv4_tensor_scale(__uint_as_float(all << 16));
+  }
 }
 
-__global__ void tensor_scale_kernel(float *ts) { *ts = nv4_tensor_scale(*ts); }
-
-// Decode: a thread turns 8 codes (one 4-byte load) into 8 bf16.
+// Decode: a thread turns kPer groups of 8 codes (4 bytes each) into bf16.
 template <int FMT>
 __global__ void __launch_bounds__(256)
     unpack_f4_kernel(const uint32_t *__restrict__ codes,
                      const uint8_t *__restrict__ scales,
                      const float *__restrict__ ts, int64_t units,
                      uint4 *__restrict__ out, int32_t *status) {
+  pdl_launch_dependents();
+  pdl_wait();
   const float g = FMT == TQ_FMT_NV4 && ts != nullptr ? *ts : 1.0f;
   bool bad = false;
-  for (int64_t u = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; u < units;
-       u += (int64_t)gridDim.x * blockDim.x) {
-    const uint32_t w = __ldg(codes + u);
-    const uint32_t b = __ldg(scales + u / (f4_block(FMT) / 8));
-    if (FMT == TQ_FMT_NV4 && (b & 0x80u)) bad = true;
-    const float s = f4_scale<FMT>(b);
-    uint32_t h[4], o[4];
-    f4x8_to_h2(w, h);
+  for (int64_t u0 = (int64_t)blockIdx.x * kChunk + threadIdx.x; u0 < units;
+       u0 += (int64_t)gridDim.x * kChunk) {
+    uint32_t w[kPer], b[kPer];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float2 f = __half22float2(*reinterpret_cast<__half2 *>(&h[i]));
-      f.x *= s;  // exact: 2 significant bits times 1 or 4
-      f.y *= s;
-      if (FMT == TQ_FMT_NV4) {
-        f.x *= g;
-        f.y *= g;
+    for (int i = 0; i < kPer; ++i) {
+      const int64_t u = u0 + 256 * i;
+      w[i] = b[i] = 0;
+      if (u < units) {
+        w[i] = __ldg(codes + u);
+        b[i] = __ldg(scales + u / (f4_block(FMT) / 8));
       }
-      const __nv_bfloat162 p = __floats2bfloat162_rn(f.x, f.y);
-      o[i] = *reinterpret_cast<const uint32_t *>(&p);
     }
-    __stcs(out + u, make_uint4(o[0], o[1], o[2], o[3]));
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int64_t u = u0 + 256 * i;
+      if (FMT == TQ_FMT_NV4 && (b[i] & 0x80u)) bad = true;
+      const float s = f4_scale<FMT>(b[i]);
+      uint32_t h[4], o[4];
+      f4x8_to_h2(w[i], h);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float2 f = __half22float2(*reinterpret_cast<__half2 *>(&h[j]));
+        f.x *= s;  // exact: 2 significant bits times 1 or 4
+        f.y *= s;
+        if (FMT == TQ_FMT_NV4) {
+          f.x *= g;
+          f.y *= g;
+        }
+        const __nv_bfloat162 p = __floats2bfloat162_rn(f.x, f.y);
+        o[j] = *reinterpret_cast<const uint32_t *>(&p);
+      }
+      if (u < units) __stcs(out + u, make_uint4(o[0], o[1], o[2], o[3]));
+    }
   }
   if (bad) report(status, TQ_ERR_BAD_CODE);
 }
 
-cudaError_t grid_for(int64_t units, int per_sm, int *grid) {
+// Blocks for `units` units of each of `rows` rows, 8 per SM at most.
+cudaError_t grid_for(int64_t rows, int64_t units, dim3 *grid) {
   int dev = 0, sms = 148;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const int64_t want = (units + 255) / 256;
-  *grid = (int)(want < (int64_t)sms * per_sm ? want : (int64_t)sms * per_sm);
+  const int64_t want = (units + kChunk - 1) / kChunk, most = (int64_t)sms * 8;
+  const int64_t x = want < most ? want : most;
+  const int64_t y = rows < most / x ? rows : most / x;
+  *grid = dim3((unsigned)x, (unsigned)(y < 1 ? 1 : y));
   return cudaSuccess;
 }
 
@@ -297,52 +375,54 @@ cudaError_t launch_quantize_f4(const uint16_t *W, int64_t n, int64_t k,
                                int64_t ldw, int format, uint8_t *codes,
                                uint8_t *scales, float *ts, bool given,
                                int32_t *status, cudaStream_t stream) {
-  const int64_t units = n * (k / 8);
   const bool own_scale = format == TQ_FMT_NV4 && !given;
-  if (units == 0 && !own_scale) return cudaSuccess;
-  int grid = 1;
-  cudaError_t e = grid_for(units, 16, &grid);
-  if (e != cudaSuccess) return e;
+  if (n == 0 || k == 0) {
+    if (!own_scale) return cudaSuccess;
+    static const float one = 1.0f;  // of an empty matrix
+    return cudaMemcpyAsync(ts, &one, sizeof(one), cudaMemcpyHostToDevice,
+                           stream);
+  }
+  const bool dense = ldw == k || n == 1;
+  const int64_t rows = dense ? 1 : n, units = dense ? n * (k / 8) : k / 8;
+  const uint4 *src = reinterpret_cast<const uint4 *>(W);
   uint32_t *c = reinterpret_cast<uint32_t *>(codes);
+  dim3 grid;
+  cudaError_t e = grid_for(rows, units, &grid);
+  if (e != cudaSuccess) return e;
   if (own_scale) {
-    if ((e = cudaMemsetAsync(ts, 0, sizeof(float), stream)) != cudaSuccess)
+    // the front of the codes, not written yet, is the maximum's scratch
+    if ((e = cudaMemsetAsync(codes, 0, 8, stream)) != cudaSuccess) return e;
+    if ((e = launch_pdl(amax_f4_kernel, grid, dim3(256), 0, stream, src, rows,
+                        units, ldw / 8, c, ts)) != cudaSuccess)
       return e;
-    if (units > 0) {
-      amax_f4_kernel<<<grid, 256, 0, stream>>>(
-          W, units, k / 8, ldw, reinterpret_cast<uint32_t *>(ts));
-      if ((e = cudaGetLastError()) != cudaSuccess) return e;
-      quantize_f4_kernel<TQ_FMT_NV4, true><<<grid, 256, 0, stream>>>(
-          W, units, k / 8, ldw, c, scales, ts, status);
-      if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    }
-    tensor_scale_kernel<<<1, 1, 0, stream>>>(ts);
-    return cudaGetLastError();
+    return launch_pdl(quantize_f4_kernel<TQ_FMT_NV4>, grid, dim3(256), 0,
+                      stream, src, rows, units, ldw / 8, c, scales,
+                      (const float *)ts, status);
   }
   if (format == TQ_FMT_NV4)
-    quantize_f4_kernel<TQ_FMT_NV4, false><<<grid, 256, 0, stream>>>(
-        W, units, k / 8, ldw, c, scales, ts, status);
-  else
-    quantize_f4_kernel<TQ_FMT_MX4, false><<<grid, 256, 0, stream>>>(
-        W, units, k / 8, ldw, c, scales, ts, status);
-  return cudaGetLastError();
+    return launch_pdl(quantize_f4_kernel<TQ_FMT_NV4>, grid, dim3(256), 0,
+                      stream, src, rows, units, ldw / 8, c, scales,
+                      (const float *)ts, status);
+  return launch_pdl(quantize_f4_kernel<TQ_FMT_MX4>, grid, dim3(256), 0,
+                    stream, src, rows, units, ldw / 8, c, scales,
+                    (const float *)nullptr, status);
 }
 
 cudaError_t launch_unpack_f4(const WeightsView &w, uint16_t *out,
                              int32_t *status, cudaStream_t stream) {
   const int64_t units = w.n * (w.k / 8);
-  int grid = 1;
-  const cudaError_t e = grid_for(units, 16, &grid);
+  dim3 grid;
+  const cudaError_t e = grid_for(1, units, &grid);
   if (e != cudaSuccess) return e;
   const uint32_t *c = reinterpret_cast<const uint32_t *>(w.codes);
   const uint8_t *s = reinterpret_cast<const uint8_t *>(w.scales);
   uint4 *o = reinterpret_cast<uint4 *>(out);
-  if (w.format == TQ_FMT_MX4)
-    unpack_f4_kernel<TQ_FMT_MX4><<<grid, 256, 0, stream>>>(c, s, nullptr,
-                                                           units, o, status);
-  else
-    unpack_f4_kernel<TQ_FMT_NV4><<<grid, 256, 0, stream>>>(c, s, w.lut, units,
-                                                           o, status);
-  return cudaGetLastError();
+  return w.format == TQ_FMT_MX4
+             ? launch_pdl(unpack_f4_kernel<TQ_FMT_MX4>, grid, dim3(256), 0,
+                          stream, c, s, (const float *)nullptr, units, o,
+                          status)
+             : launch_pdl(unpack_f4_kernel<TQ_FMT_NV4>, grid, dim3(256), 0,
+                          stream, c, s, w.lut, units, o, status);
 }
 
 }  // namespace tq

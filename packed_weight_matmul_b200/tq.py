@@ -125,7 +125,8 @@ def _ptr(t):
 
 def _stream(stream):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # torch.cuda.current_stream().cuda_stream without the object (2 us)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return stream
@@ -401,8 +402,7 @@ def _f4_tensor(t, dtypes, what):
     """The 4-bit entry points check what the C ABI cannot see of a tensor:
     that it lies on the current device, with the element type it is read as
     and dense rows."""
-    if t.device.type != "cuda" or \
-            t.device.index != torch.cuda.current_device():
+    if not t.is_cuda or t.get_device() != torch._C._cuda_getDevice():
         raise TqError(TQ_ERR_INVALID_ARG, f"{what}: not on the current device")
     if t.dtype not in dtypes:
         raise TqError(TQ_ERR_INVALID_ARG, f"{what}: {t.dtype}")

@@ -89,7 +89,7 @@ BAD_DESC = [
     (dict(format=9), "INVALID_ARG"), (dict(group=32), "UNSUPPORTED"),
     (dict(format=4, group=16), "UNSUPPORTED"),
     (dict(format=4, lut=0x30000), "INVALID_ARG"),
-    (dict(k_cols=48), "SHAPE"), (dict(codes=0x10008), "ALIGNMENT"),
+    (dict(k_cols=1 << 28), "UNSUPPORTED"), (dict(k_cols=48), "SHAPE"), (dict(codes=0x10008), "ALIGNMENT"),
     (dict(scales=0x20004), "ALIGNMENT"), (dict(lut=0x30002), "ALIGNMENT"),
 ]
 
