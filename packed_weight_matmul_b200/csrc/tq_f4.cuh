@@ -44,6 +44,15 @@ __device__ __forceinline__ float f4_scale(uint32_t b) {
   return FMT == TQ_FMT_MX4 ? e8m0_to_f32(b) : e4m3_to_f32(b);
 }
 
+// All threads of a cluster meet. Relaxed: it orders no memory (the ordinary
+// barrier waits until this CTA's global stores are acknowledged, about 1 us),
+// which is enough where CTAs only tell one another that they have finished
+// reading.
+__device__ __forceinline__ void cluster_sync_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed;\n"
+               "barrier.cluster.wait;" ::: "memory");
+}
+
 cudaError_t launch_quantize_f4(const uint16_t *W, int64_t n, int64_t k,
                                int64_t ldw, int format, uint8_t *codes,
                                uint8_t *scales, float *tensor_scale,
@@ -60,12 +69,24 @@ cudaError_t launch_linear_experts_f4(const WeightsView &w, int n_experts,
                                      const __nv_bfloat16 *x, int64_t ldx,
                                      float *y, int64_t ldy, int32_t *status,
                                      cudaStream_t stream);
-// y = x W^T, both in 4 bits: up to 16 rows of x on the row kernel, more on the
-// block-scaled tensor cores.
-bool rows_f4_packed_supported(const WeightsView &x);
-cudaError_t rows_f4_packed(const WeightsView &w, const WeightsView &x, void *y,
-                           int64_t ldy, int y_type, cudaStream_t stream);
+// y = x W^T, both in 4 bits.
 cudaError_t launch_linear_f4(const WeightsView &w, const WeightsView &x,
+                             void *y, int64_t ldy, int y_type,
+                             cudaStream_t stream);
+
+// Few rows of x on the block-scaled tensor cores (tq_f4_decode.cu): bf16 rows,
+// rows that pick an expert, packed rows. `copies` matrices of w.n rows lie
+// behind one another.
+bool decode_f4_supported(const WeightsView &w, int64_t copies);
+cudaError_t decode_f4_bf16(const WeightsView &w, const __nv_bfloat16 *x,
+                           int64_t batch, int64_t ldx, float *y, int64_t ldy,
+                           cudaStream_t stream);
+cudaError_t decode_f4_experts(const WeightsView &w, int n_experts,
+                              const int32_t *ids, int64_t tokens,
+                              const __nv_bfloat16 *x, int64_t ldx, float *y,
+                              int64_t ldy, int32_t *status,
+                              cudaStream_t stream);
+cudaError_t decode_f4_packed(const WeightsView &w, const WeightsView &x,
                              void *y, int64_t ldy, int y_type,
                              cudaStream_t stream);
 

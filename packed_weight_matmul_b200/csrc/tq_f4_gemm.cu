@@ -31,21 +31,15 @@
 //
 // Every wait is bounded; one that gives up leaves NaN in the outputs of the
 // tiles that were not finished.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
-#include <mutex>
-
-#include "tq_f4.cuh"
-#include "tq_sm100_async.cuh"
-#include "tq_sm100_mma.cuh"
+#include "tq_f4_tc.cuh"
 
 namespace tq {
+using namespace f4;
 namespace {
 
 constexpr int kThreads = 576;
 constexpr int kRowsM = 128;         // weight rows per CTA
-constexpr uint32_t kStageRow = 128; // code bytes of a row per stage (256 k)
+constexpr uint32_t kStageRow = kF4StageRow;
 constexpr uint32_t kTmemColumns = 512;
 constexpr uint32_t kSmemLimit = 227u * 1024u;
 constexpr int kScaleWarps = 4, kScaleGroups = 2, kDrainWarps = 8;
@@ -95,14 +89,6 @@ struct Args {
   int k, tiles_m, tiles_n, y_bf16;
 };
 
-__device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t a, uint32_t b,
-                                         uint32_t c, uint32_t d) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::
-                   "r"(taddr),
-               "r"(a), "r"(b), "r"(c), "r"(d)
-               : "memory");
-}
-
 template <int CG>
 __device__ __forceinline__ void alloc_columns(uint32_t dst, uint32_t cols) {
   if constexpr (CG == 1) {
@@ -127,173 +113,6 @@ __device__ __forceinline__ void free_columns(uint32_t taddr, uint32_t cols) {
                      taddr),
                  "r"(cols)
                  : "memory");
-}
-
-// Whether the phase of parity `parity` is over, without waiting; for a pair
-// with acquire at cluster scope.
-template <int CG>
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  if constexpr (CG == 1)
-    asm volatile(
-        "{\n .reg .pred p;\n"
-        " mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-        " selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-  else
-    asm volatile(
-        "{\n .reg .pred p;\n"
-        " mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], "
-        "%2;\n selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-  return ok != 0;
-}
-
-#define TQ_COMMIT_1                                                          \
-  "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64"
-#define TQ_COMMIT_2                                                          \
-  "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster."       \
-  "multicast::cluster.b64"
-
-// Arrive on `bar` (of both CTAs of a pair) when all MMAs issued so far are
-// complete. Whole warp; the elected lane is the one that issues the MMAs.
-template <int CG>
-__device__ __forceinline__ void commit(uint32_t bar) {
-  if constexpr (CG == 1)
-    asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xFFFFFFFF;\n"
-                 " @q " TQ_COMMIT_1 " [%0];\n}" ::"r"(bar)
-                 : "memory");
-  else
-    asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xFFFFFFFF;\n"
-                 " @q " TQ_COMMIT_2 " [%0], %1;\n}" ::"r"(bar),
-                 "h"((uint16_t)3)
-                 : "memory");
-}
-
-// One stage: D (+)= (A * scale A)(B * scale B)^T over 4 x 64 k, then arrive
-// on `bar` as commit does. id0 / id1 are the instruction descriptors of even
-// and odd MMAs, whose scale words start at sa + 4 w and sb + bcols w, w = j
-// (NV4) or j / 2 (MX4). The whole warp comes here together and one elected
-// lane issues: that way the operands stay in uniform registers (issued from
-// inside an `if (lane == 0)`, an MMA cost about 80 cycles of moving them
-// there, more than the tensor core needed for it).
-template <int FMT, int CG>
-__device__ __forceinline__ void mma_stage(uint32_t d, uint64_t a, uint64_t b,
-                                          uint32_t id0, uint32_t id1,
-                                          uint32_t sa, uint32_t sb,
-                                          uint32_t bcols, uint32_t accumulate,
-                                          uint32_t bar) {
-  constexpr uint32_t kW = FMT == TQ_FMT_NV4 ? 1u : 0u;
-  const uint32_t sa1 = sa + 4 * kW, sb1 = sb + bcols * kW;
-  const uint32_t sa2 = sa + 4 * (1 + kW), sb2 = sb + bcols * (1 + kW);
-  const uint32_t sa3 = sa2 + 4 * kW, sb3 = sb2 + bcols * kW;
-#define TQ_MMA(KIND, DA, DB, ID, SA, SB, P)                                   \
-  " @q tcgen05.mma.cta_group::" KIND " [%0], " DA ", " DB ", " ID ", [" SA     \
-  "], [" SB "], " P ";\n"
-#define TQ_STAGE(KIND, COMMIT)                                                \
-  asm volatile(                                                               \
-      "{\n .reg .pred p, q, t;\n .reg .b64 a1, a2, a3, b1, b2, b3;\n"         \
-      " elect.sync _|q, 0xFFFFFFFF;\n setp.ne.b32 p, %13, 0;\n"               \
-      " setp.eq.b32 t, 0, 0;\n"                                               \
-      " add.s64 a1, %1, 2;\n add.s64 a2, %1, 4;\n add.s64 a3, %1, 6;\n"       \
-      " add.s64 b1, %2, 2;\n add.s64 b2, %2, 4;\n add.s64 b3, %2, 6;\n"       \
-      TQ_MMA(KIND, "%1", "%2", "%3", "%5", "%9", "p")                         \
-      TQ_MMA(KIND, "a1", "b1", "%4", "%6", "%10", "t")                        \
-      TQ_MMA(KIND, "a2", "b2", "%3", "%7", "%11", "t")                        \
-      TQ_MMA(KIND, "a3", "b3", "%4", "%8", "%12", "t")                        \
-      " @q " COMMIT ";\n}" ::"r"(d),                                          \
-      "l"(a), "l"(b), "r"(id0), "r"(id1), "r"(sa), "r"(sa1), "r"(sa2),        \
-      "r"(sa3), "r"(sb), "r"(sb1), "r"(sb2), "r"(sb3), "r"(accumulate),       \
-      "r"(bar), "h"((uint16_t)3)                                              \
-      : "memory")
-  if constexpr (FMT == TQ_FMT_MX4 && CG == 1)
-    TQ_STAGE("1.kind::mxf4.block_scale.scale_vec::2X", TQ_COMMIT_1 " [%14]");
-  else if constexpr (FMT == TQ_FMT_MX4)
-    TQ_STAGE("2.kind::mxf4.block_scale.scale_vec::2X",
-             TQ_COMMIT_2 " [%14], %15");
-  else if constexpr (CG == 1)
-    TQ_STAGE("1.kind::mxf4nvf4.block_scale.scale_vec::4X",
-             TQ_COMMIT_1 " [%14]");
-  else
-    TQ_STAGE("2.kind::mxf4nvf4.block_scale.scale_vec::4X",
-             TQ_COMMIT_2 " [%14], %15");
-#undef TQ_STAGE
-#undef TQ_MMA
-}
-
-// Instruction descriptor of the 4-bit kinds: scale byte of B at bits 4-5 and
-// of A at 29-30 (first of the word's bytes that this MMA uses), E2M1 = 1 at
-// 7-9 and 10-12, N >> 3 at 17-22, E8M0 scales at 23, M >> 4 at 24-28.
-template <int FMT>
-__host__ __device__ constexpr uint32_t idesc_f4(int M, int N, uint32_t byte) {
-  return (byte << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) |
-         ((FMT == TQ_FMT_MX4 ? 1u : 0u) << 23) | ((uint32_t)(M >> 4) << 24) |
-         (byte << 29);
-}
-
-__device__ __forceinline__ void bar_sync(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
-// One piece (8 or 16 scale bytes) of a row at `off`, `left` bytes before the
-// row's end; bytes past it are 0 (their codes are zero too).
-template <int WORDS>
-__device__ __forceinline__ void load_piece(uint32_t (&v)[WORDS],
-                                           const uint8_t *p, int left) {
-#pragma unroll
-  for (int w = 0; w < WORDS; ++w) v[w] = 0;
-  if (left <= 0) return;
-  if constexpr (WORDS == 2) {
-    const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p));
-    v[0] = u.x;
-    v[1] = u.y;
-  } else {
-    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
-    v[0] = u.x;
-    v[1] = u.y;
-    v[2] = u.z;
-    v[3] = u.w;
-  }
-}
-
-// The same byte by byte, for rows that do not start on a piece's boundary.
-template <int WORDS>
-__device__ __forceinline__ void load_piece_bytes(uint32_t (&v)[WORDS],
-                                                 const uint8_t *p, int left) {
-#pragma unroll
-  for (int w = 0; w < WORDS; ++w) {
-    uint32_t x = 0;
-#pragma unroll 1
-    for (int b = 0; b < 4 && 4 * w + b < left; ++b)
-      x |= (uint32_t)__ldg(p + 4 * w + b) << (8 * b);
-    v[w] = x;
-  }
-}
-
-template <int WORDS>
-__device__ __forceinline__ void store_piece(uint32_t at,
-                                            const uint32_t (&v)[WORDS]) {
-  if constexpr (WORDS == 2)
-    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(v[0]),
-                 "r"(v[1])
-                 : "memory");
-  else
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at),
-                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
-                 : "memory");
-}
-
-// Where piece c of row r's unit (PIECES of BYTES bytes) lies in a group's
-// scale buffer: row after row, a row's pieces swapped so that the reads of
-// one piece by consecutive rows hit different banks.
-template <uint32_t PIECES, uint32_t BYTES>
-__device__ __forceinline__ uint32_t scale_at(uint32_t r, uint32_t c) {
-  constexpr uint32_t kRowsPer128 = 128u / (PIECES * BYTES);
-  return (r * PIECES + (c ^ ((r / kRowsPer128) & (PIECES - 1)))) * BYTES;
 }
 
 // Two accumulator columns times g as bf16, `lo` in the low half.
@@ -686,38 +505,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault,
-                                &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  });
-  return fn;
-}
-
-// Packed codes [rows][k/2]; boxes of 128 bytes (256 k) x `box` rows, 128-byte
-// swizzle. Rows and columns past the matrix read as zero codes.
-cudaError_t code_map(CUtensorMap *map, const WeightsView &w, int box_rows) {
-  auto encode = encode_fn();
-  if (encode == nullptr) return cudaErrorNotSupported;
-  const cuuint64_t dims[2] = {(cuuint64_t)(w.k / 2), (cuuint64_t)w.n};
-  const cuuint64_t strides[1] = {(cuuint64_t)(w.k / 2)};
-  const cuuint32_t box[2] = {kStageRow, (cuuint32_t)box_rows};
-  const cuuint32_t estr[2] = {1u, 1u};
-  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
-                const_cast<uint8_t *>(w.codes), dims, strides, box, estr,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-             ? cudaSuccess
-             : cudaErrorInvalidValue;
-}
-
 template <int FMT, int NT, int CG>
 cudaError_t launch(const WeightsView &w, const WeightsView &x, void *y,
                    int64_t ldy, int y_type, cudaStream_t stream) {
@@ -793,8 +580,8 @@ cudaError_t dispatch(const WeightsView &w, const WeightsView &x, void *y,
 cudaError_t launch_linear_f4(const WeightsView &w, const WeightsView &x,
                              void *y, int64_t ldy, int y_type,
                              cudaStream_t stream) {
-  if (rows_f4_packed_supported(x))
-    return rows_f4_packed(w, x, y, ldy, y_type, stream);
+  if (x.n <= 64 && decode_f4_supported(w, 1))
+    return decode_f4_packed(w, x, y, ldy, y_type, stream);
   return w.format == TQ_FMT_MX4
              ? dispatch<TQ_FMT_MX4>(w, x, y, ldy, y_type, stream)
              : dispatch<TQ_FMT_NV4>(w, x, y, ldy, y_type, stream);

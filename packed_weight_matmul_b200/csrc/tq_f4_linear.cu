@@ -2,8 +2,8 @@
 //
 //   y[b][n] = g sum_k c[n][k] s[n][k / B] x[b][k]
 //
-// for bf16 x (tq_linear), for rows of x that pick their matrix
-// (tq_linear_experts_f4) and for up to 16 rows of 4-bit x (tq_linear_f4).
+// for bf16 x (tq_linear) and for rows of x that pick their matrix
+// (tq_linear_experts_f4).
 // Bound by the codes' way from HBM (0.53 bytes per weight), so a weight may
 // cost about 3 lane instructions.
 //
@@ -33,7 +33,6 @@
 // takes 16 consecutive bytes (32 codes) of rows g and g + 8, and its part of
 // an x row is the same 32 k, 8 per 16-byte load.
 #include <cooperative_groups.h>
-#include <stdlib.h>
 
 #include "tq_f4_rows.cuh"
 
@@ -41,26 +40,17 @@ namespace tq {
 namespace {
 
 constexpr int kStageK = 256;    // codes of a row per stage
-constexpr int kRing = 3;        // stages of a warp's ring
-constexpr int kSegment = 2048;  // ids looked through at once
+constexpr int kSegment = 1024;  // ids looked through at once
 constexpr int kPrefetch = 1024; // bytes of a row hinted to the L2 cache
-
-static int g_force_ks = getenv("FORCE_KS") ? atoi(getenv("FORCE_KS")) : 0;
-// Where the rows of x come from.
-enum { kBf16 = 0, kPacked = 1 };
 
 struct RowArgs {
   const uint8_t *codes, *scales;  // weights (of expert 0)
   const float *g;                 // tensor scale(s) or null
   int64_t n, k;
-  const __nv_bfloat16 *x;  // kBf16
-  int64_t ldx;
-  const uint8_t *xcodes, *xscales;  // kPacked
-  const float *xg;
-  int64_t batch;
-  void *y;
+  const __nv_bfloat16 *x;
+  int64_t ldx, batch;
+  float *y;
   int64_t ldy;
-  int y_bf16;
   const int32_t *ids;  // null: one matrix, rows of x in order
   int n_experts;
   int32_t *status;
@@ -69,40 +59,28 @@ struct RowArgs {
 
 template <int FMT, int NT>
 struct RowPlan {
-  // 8 warps, two CTAs per SM; 64 rows of x share one large CTA instead
-  static constexpr int kWarps = NT == 64 ? 16 : 8;
-  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kWarps = 8, kThreads = 32 * kWarps;
   static constexpr int kTile = 16 * kWarps;  // weight rows of a CTA
+  static constexpr int kCtas = NT <= 16 ? 3 : 2;  // per SM
+  static constexpr int kRing = NT <= 16 ? 2 : 3;  // stages of a warp's ring
+  // buffers of x: with 64 rows there is room for one only
+  static constexpr int kXBufs = NT == 64 ? 1 : 2;
   static constexpr int kScaleRow = FMT == TQ_FMT_MX4 ? 8 : 16;  // per stage
   static constexpr int kScalePitch = FMT == TQ_FMT_MX4 ? 16 : 32;
   static constexpr int kCodes = 16 * kStageK / 2;
   static constexpr int kStage = kCodes + 16 * kScalePitch;
-  static constexpr int kXK = NT == 8 ? 1024 : NT == 16 ? 512 : 256;
+  static constexpr int kXK = NT == 8 ? 512 : 256;
   static constexpr int kXStages = kXK / kStageK;
   static constexpr int kXPitch = kXK * 2 + 64;
   static constexpr int kXBuf = NT * kXPitch;
   static constexpr int kUnits = kXK / 8;  // 8-value units of a buffered x row
   static constexpr int kPer = NT * kUnits / kThreads;  // units per thread
-  static_assert(kUnits % 32 == 0 && kPer == 4, "a warp's units share a row");
+  static_assert(kUnits % 32 == 0, "a warp's units share a row");
   static constexpr int kPartPitch = kTile + 4;
   static constexpr int kRingBytes = kWarps * kRing * kStage;
   static constexpr int kPart = NT * kPartPitch * 4;
   static constexpr int kBody = kRingBytes > kPart ? kRingBytes : kPart;
-  static constexpr int kSmem = kBody + 2 * kXBuf;
-};
-
-// One lane's share of a buffer of x rows, in flight between global memory and
-// the conversion.
-template <int SRC, int COUNT>
-struct XRegs;
-template <int COUNT>
-struct XRegs<kBf16, COUNT> {
-  uint4 v[COUNT];
-};
-template <int COUNT>
-struct XRegs<kPacked, COUNT> {
-  uint32_t v[COUNT];  // 8 codes
-  uint32_t s[COUNT];  // their scale byte
+  static constexpr int kSmem = kBody + kXBufs * kXBuf;
 };
 
 __device__ __forceinline__ uint32_t max_mag8(const uint4 &w) {
@@ -132,30 +110,16 @@ __device__ __forceinline__ uint32_t scaled_h2(uint32_t w, float s) {
   return r;
 }
 
-// fp16 pair of the MX4 factor 2^(E - R + 13): exponent field E - R + 28.
-__device__ __forceinline__ uint32_t mx4_factor(int E, int R) {
-  const int f = E - R + 28;
-  const uint32_t h = f > 0 ? (uint32_t)f : 0u;
-  return E == 255 ? 0x7E007E00u : h * 0x04000400u;
-}
-
-// fp16 pair of an E4M3 byte (its sign is not looked at).
-__device__ __forceinline__ uint32_t nv4_factor(uint32_t b) {
-  uint32_t h;
-  b &= 0x7Fu;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(b | b << 8)));
-  return h;
-}
-
 // WHOLE: k is a multiple of 256, so that every row's scale bytes start aligned
 // and no stage is cut short.
-template <int FMT, int NT, int SRC, bool WHOLE>
+template <int FMT, int NT, bool WHOLE>
 __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
-                                  NT == 64 ? 1 : 2)
+                                  RowPlan<FMT, NT>::kCtas)
     rows_f4_kernel(const RowArgs a) {
   using P = RowPlan<FMT, NT>;
   constexpr int kWarps = P::kWarps, kThreads = P::kThreads, kTile = P::kTile;
   constexpr int kTiles = NT / 8;  // mma columns
+  constexpr int kRing = P::kRing;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int s_rows[kSegment];
   __shared__ int s_count[kSegment / 32 + 1];
@@ -259,10 +223,10 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
     uint32_t R = 0;  // MX4: R of row g in the low half, of row g + 8 above
-    // X (bf16) or R (MX4 x) of the rows of this thread's units
+    // X of the rows of this thread's units
     int ex[P::kPer];
 #pragma unroll
-    for (int j = 0; j < P::kPer; ++j) ex[j] = SRC == kBf16 ? -112 : 0;
+    for (int j = 0; j < P::kPer; ++j) ex[j] = -112;
 
 #pragma unroll 1
     for (int p = 0; p < kRing - 1; ++p) issue(p, p);
@@ -272,114 +236,112 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
     const int64_t k_end =
         (int64_t)st1 * kStageK < a.k ? (int64_t)st1 * kStageK : a.k;
     const int buffers = (count + P::kXStages - 1) / P::kXStages;
-    XRegs<SRC, P::kPer> xr;
-    auto load_x = [&](int i) {
+    constexpr int kHeld = P::kPer < 4 ? P::kPer : 4;  // units in registers
+    uint4 xr[kHeld];
+    auto load_x = [&](int i, int j0) {
       if (i >= buffers) return;
       const int64_t k0 = (int64_t)st0 * kStageK + (int64_t)i * P::kXK;
 #pragma unroll
-      for (int j = 0; j < P::kPer; ++j) {
-        const int q = tid + kThreads * j, r = q / P::kUnits;
+      for (int j = 0; j < kHeld; ++j) {
+        const int q = tid + kThreads * (j0 + j), r = q / P::kUnits;
         const int64_t k = k0 + 8 * (q % P::kUnits);
         const bool live = r < rows && k < k_end;
         const int64_t row =
             !live ? 0 : a.ids != nullptr ? s_rows[base + r] : b0 + r;
-        if constexpr (SRC == kBf16) {
-          xr.v[j] = make_uint4(0, 0, 0, 0);
-          if (live)
-            xr.v[j] =
-                __ldg(reinterpret_cast<const uint4 *>(a.x + row * a.ldx + k));
-        } else {
-          xr.v[j] = 0;
-          xr.s[j] = 0;
-          if (live) {
-            xr.v[j] = __ldg(reinterpret_cast<const uint32_t *>(
-                a.xcodes + row * code_pitch + k / 2));
-            xr.s[j] = __ldg(a.xscales + row * blocks + k / f4_block(FMT));
-          }
-        }
+        xr[j] = make_uint4(0, 0, 0, 0);
+        if (live)
+          xr[j] = __ldg(reinterpret_cast<const uint4 *>(a.x + row * a.ldx + k));
       }
     };
-    // The largest magnitude (bf16 bits) or scale byte of each warp's units.
-    constexpr bool kHasExp = SRC == kBf16 || FMT == TQ_FMT_MX4;
+    // The largest magnitude (bf16 bits) of a warp's units.
+    constexpr bool kShared = P::kUnits > 32;  // a row's units lie in two warps
+    auto warp_max = [&](int j) {
+      uint32_t m = __reduce_max_sync(0xFFFFFFFFu, max_mag8(xr[j]));
+      if (m >= 0x7F80u)  // NaN or Inf: take the largest finite value
+        m = __reduce_max_sync(0xFFFFFFFFu, max_finite8(xr[j]));
+      return m;
+    };
     auto publish = [&](int i) {
-      if (!kHasExp || i >= buffers) return;
+      if (!kShared || i >= buffers) return;
 #pragma unroll
-      for (int j = 0; j < P::kPer; ++j) {
+      for (int j = 0; j < kHeld; ++j) {
         if ((warp * 32 + kThreads * j) / P::kUnits >= rows) break;
-        uint32_t m;
-        if constexpr (SRC == kBf16) {
-          m = __reduce_max_sync(0xFFFFFFFFu, max_mag8(xr.v[j]));
-          if (m >= 0x7F80u)  // NaN or Inf: take the largest finite value
-            m = __reduce_max_sync(0xFFFFFFFFu, max_finite8(xr.v[j]));
-        } else {
-          const uint32_t b = xr.s[j];
-          m = __reduce_max_sync(0xFFFFFFFFu, b == 255u ? 0u : b);
-        }
+        const uint32_t m = warp_max(j);
         if (lane == 0) s_max[i & 1][warp + kWarps * j] = m;
       }
     };
-    // registers -> fp16 in buffer i & 1; whether a row's exponent rose
-    auto convert = [&](int i) {
+    // registers -> fp16 in buffer i; whether a row's exponent rose
+    auto convert = [&](int i, int j0) {
       bool rose = false;
       if (i >= buffers) return rose;
 #pragma unroll
-      for (int j = 0; j < P::kPer; ++j) {
-        const int q = tid + kThreads * j, r = q / P::kUnits;
-        if ((warp * 32 + kThreads * j) / P::kUnits >= rows) break;
+      for (int j = 0; j < kHeld; ++j) {
+        const int q = tid + kThreads * (j0 + j), r = q / P::kUnits;
+        if ((warp * 32 + kThreads * (j0 + j)) / P::kUnits >= rows) break;
         const int unit = q % P::kUnits;
-        if (kHasExp) {
-          uint32_t m = 0;
+        int &x_exp = ex[j0 + j];
+        uint32_t m = 0;
+        if constexpr (kShared) {
 #pragma unroll
           for (int u = 0; u < P::kUnits / 32; ++u)
             m = max(m, s_max[i & 1][r * (P::kUnits / 32) + u]);
-          const int now =
-              max(ex[j], SRC == kBf16 ? (int)(m >> 7) - 127 : (int)m);
-          if (unit == 0) s_fac[i & 1][r] = pow2_down(ex[j] - now);
-          rose |= now != ex[j];
-          ex[j] = now;
-        }
-        uint4 h;
-        if constexpr (SRC == kBf16) {
-          // 2^(14 - X), X >= -112
-          const float f = __uint_as_float((uint32_t)(141 - ex[j]) << 23);
-          h.x = scaled_h2(xr.v[j].x, f);
-          h.y = scaled_h2(xr.v[j].y, f);
-          h.z = scaled_h2(xr.v[j].z, f);
-          h.w = scaled_h2(xr.v[j].w, f);
         } else {
-          uint32_t c[4];
-          f4x8_to_h2(xr.v[j], c);
-          const uint32_t f = FMT == TQ_FMT_MX4 ? mx4_factor((int)xr.s[j], ex[j])
-                                               : nv4_factor(xr.s[j]);
-          h = make_uint4(hmul2(c[0], f), hmul2(c[1], f), hmul2(c[2], f),
-                         hmul2(c[3], f));
+          m = warp_max(j);
         }
+        const int now = max(x_exp, (int)(m >> 7) - 127);
+        if (unit == 0) s_fac[i & 1][r] = pow2_down(x_exp - now);
+        rose |= now != x_exp;
+        x_exp = now;
+        // 2^(14 - X), X >= -112
+        const float f = __uint_as_float((uint32_t)(141 - x_exp) << 23);
+        const uint4 h =
+            make_uint4(scaled_h2(xr[j].x, f), scaled_h2(xr[j].y, f),
+                       scaled_h2(xr[j].z, f), scaled_h2(xr[j].w, f));
         // unit 4 t + s of a group of 128 k lies at position 4 s + t, so that
         // the four lanes of a quad read 64 consecutive bytes
         const int pos = (unit & ~15) | ((unit & 3) << 2) | ((unit >> 2) & 3);
-        sts128(xbuf + (i & 1) * P::kXBuf + r * P::kXPitch + pos * 16, h);
+        sts128(xbuf + (P::kXBufs == 2 ? i & 1 : 0) * P::kXBuf +
+                   r * P::kXPitch + pos * 16,
+               h);
       }
       return rose;
     };
 
-    load_x(0);
-    for (int i = tid; i < 2 * (NT - rows) * (P::kXPitch / 16); i += kThreads) {
+    if (P::kXBufs == 2) load_x(0, 0);
+    for (int i = tid; i < P::kXBufs * (NT - rows) * (P::kXPitch / 16);
+         i += kThreads) {
       const int b = i / ((NT - rows) * (P::kXPitch / 16));
       sts128(xbuf + b * P::kXBuf + rows * P::kXPitch +
                  (i - b * (NT - rows) * (P::kXPitch / 16)) * 16,
              make_uint4(0, 0, 0, 0));  // rows that are not there
     }
-    publish(0);
-    __syncthreads();
-    int any = convert(0);
-    load_x(1);
-    publish(1);
-    any = __syncthreads_or(any);
+    int any = 0;
+    if constexpr (P::kXBufs == 2) {
+      publish(0);
+      if (kShared) __syncthreads();
+      any = convert(0, 0);
+      load_x(1, 0);
+      publish(1);
+      any = __syncthreads_or(any);
+    }
     int st = 0, slot = 0;
 #pragma unroll 1
     for (int i = 0; i < buffers; ++i) {
-      const int rose = convert(i + 1);
-      load_x(i + 2);
+      int rose = 0;
+      if constexpr (P::kXBufs == 2) {
+        rose = convert(i + 1, 0);
+        load_x(i + 2, 0);
+      } else {
+        // one buffer: filled between two barriers, while the other CTA of the
+        // SM computes
+        if (i > 0) __syncthreads();
+#pragma unroll
+        for (int j = 0; j < P::kPer; j += kHeld) {
+          load_x(i, j);
+          rose |= convert(i, j);
+        }
+        any = __syncthreads_or(rose);
+      }
       if (any) {
 #pragma unroll
         for (int c = 0; c < kTiles; ++c) {
@@ -392,7 +354,8 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
         }
       }
       const int end = st + P::kXStages < count ? st + P::kXStages : count;
-      uint32_t xat = xbuf + (i & 1) * P::kXBuf + g * P::kXPitch + t * 16;
+      uint32_t xat = xbuf + (P::kXBufs == 2 ? i & 1 : 0) * P::kXBuf +
+                     g * P::kXPitch + t * 16;
 #pragma unroll 1
       for (; st < end; ++st, xat += 2 * kStageK) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
@@ -527,8 +490,10 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
             for (int c = 0; c < 2; ++c) f[0][r][c] = f[1][r][c];
         }
       }
-      publish(i + 2);
-      any = __syncthreads_or(rose);
+      if constexpr (P::kXBufs == 2) {
+        publish(i + 2);
+        any = __syncthreads_or(rose);
+      }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll
@@ -545,12 +510,8 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int b = 8 * i + 2 * t + (j & 1);
-        int e = 0;
+        int e = s_exp[b] - 14;
         if (FMT == TQ_FMT_MX4) e += (int)(j < 2 ? R & 0xFFFFu : R >> 16) - 140;
-        if (SRC == kBf16)
-          e += s_exp[b] - 14;
-        else if (FMT == TQ_FMT_MX4)
-          e += s_exp[b] - 140;
         part[b * P::kPartPitch + 16 * warp + g + (j < 2 ? 0 : 8)] =
             scalbnf(acc[i][j], e);
       }
@@ -558,8 +519,6 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
       cooperative_groups::this_cluster().sync();
     else
       __syncthreads();
-    float gs = gw;
-    if (SRC == kPacked && a.xg != nullptr) gs *= *a.xg;
     const uint32_t mine = smem_u32(part);
     for (int i = tid + rank * kThreads; i < rows * kTile; i += ks * kThreads) {
       const int b = i / kTile, r = i % kTile;
@@ -581,19 +540,14 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
           v += u;
         }
       }
-      v *= gs;
       if (row0 + r < a.n) {
         const int64_t row = a.ids != nullptr ? s_rows[base + b] : b0 + b;
-        if (a.y_bf16)
-          static_cast<__nv_bfloat16 *>(a.y)[row * a.ldy + row0 + r] =
-              __float2bfloat16_rn(v);
-        else
-          static_cast<float *>(a.y)[row * a.ldy + row0 + r] = v;
+        a.y[row * a.ldy + row0 + r] = v * gw;
       }
     }
     // the partial tiles have been read: shared memory may change, or go
     if (ks > 1)
-      cooperative_groups::this_cluster().sync();
+      cluster_sync_relaxed();
     else
       __syncthreads();
   };
@@ -621,7 +575,7 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
         // nobody's row: NaN in this CTA's columns
         const int64_t end = row0 + kTile < a.n ? row0 + kTile : a.n;
         for (int64_t r = row0; r < end; ++r)
-          static_cast<float *>(a.y)[i * a.ldy + r] = __int_as_float(0x7FC00000);
+          a.y[i * a.ldy + r] = __int_as_float(0x7FC00000);
         report(a.status, TQ_ERR_INVALID_ARG);
       }
     }
@@ -669,7 +623,7 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
 
 // Clusters of ks CTAs that are resident together, asked once per kernel, ks
 // and device.
-template <int FMT, int NT, int SRC, bool WHOLE>
+template <int FMT, int NT, bool WHOLE>
 int resident(int ks, int dev) {
   static std::atomic<int> known[16][9];  // 0: not asked yet
   using P = RowPlan<FMT, NT>;
@@ -691,7 +645,7 @@ int resident(int ks, int dev) {
   int n = 0;
   if (cudaOccupancyMaxActiveClusters(
           &n, reinterpret_cast<const void *>(
-              rows_f4_kernel<FMT, NT, SRC, WHOLE>),
+              rows_f4_kernel<FMT, NT, WHOLE>),
           &cfg) != cudaSuccess ||
       n < 1) {
     cudaGetLastError();
@@ -702,13 +656,13 @@ int resident(int ks, int dev) {
 }
 
 // `copies`: how many row products of n rows run at once (passes, experts).
-template <int FMT, int NT, int SRC, bool WHOLE>
+template <int FMT, int NT, bool WHOLE>
 cudaError_t launch_whole(RowArgs a, int64_t copies, int64_t grid_y,
                    cudaStream_t stream) {
   using P = RowPlan<FMT, NT>;
-  auto kern = rows_f4_kernel<FMT, NT, SRC, WHOLE>;
+  auto kern = rows_f4_kernel<FMT, NT, WHOLE>;
   cudaError_t e =
-      ensure_smem_limit<rows_f4_kernel<FMT, NT, SRC, WHOLE>>(P::kSmem);
+      ensure_smem_limit<rows_f4_kernel<FMT, NT, WHOLE>>(P::kSmem);
   if (e != cudaSuccess) return e;
   int dev = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
@@ -720,11 +674,10 @@ cudaError_t launch_whole(RowArgs a, int64_t copies, int64_t grid_y,
   a.ks = 1;
   for (int ks = 8; ks > 1; --ks)
     if (2 * ks <= stages &&
-        tiles * copies <= resident<FMT, NT, SRC, WHOLE>(ks, dev)) {
+        tiles * copies <= resident<FMT, NT, WHOLE>(ks, dev)) {
       a.ks = ks;
       break;
     }
-  if (g_force_ks > 0) a.ks = g_force_ks;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * a.ks), (unsigned)grid_y);
   cfg.blockDim = dim3(P::kThreads);
@@ -742,35 +695,30 @@ cudaError_t launch_whole(RowArgs a, int64_t copies, int64_t grid_y,
   return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
-template <int FMT, int NT, int SRC>
+template <int FMT, int NT>
 cudaError_t launch(const RowArgs &a, int64_t copies, int64_t grid_y,
                    cudaStream_t stream) {
   return a.k % kStageK == 0
-             ? launch_whole<FMT, NT, SRC, true>(a, copies, grid_y, stream)
-             : launch_whole<FMT, NT, SRC, false>(a, copies, grid_y, stream);
+             ? launch_whole<FMT, NT, true>(a, copies, grid_y, stream)
+             : launch_whole<FMT, NT, false>(a, copies, grid_y, stream);
 }
 
-template <int SRC>
+template <int NT>
+cudaError_t launch_format(int format, const RowArgs &a, int64_t copies,
+                          int64_t grid_y, cudaStream_t stream) {
+  return format == TQ_FMT_MX4
+             ? launch<TQ_FMT_MX4, NT>(a, copies, grid_y, stream)
+             : launch<TQ_FMT_NV4, NT>(a, copies, grid_y, stream);
+}
+
 cudaError_t launch_nt(int format, int nt, const RowArgs &a, int64_t copies,
                       int64_t grid_y, cudaStream_t stream) {
-  const bool mx = format == TQ_FMT_MX4;
   switch (nt) {
-    case 8:
-      return mx ? launch<TQ_FMT_MX4, 8, SRC>(a, copies, grid_y, stream)
-                : launch<TQ_FMT_NV4, 8, SRC>(a, copies, grid_y, stream);
-    case 16:
-      return mx ? launch<TQ_FMT_MX4, 16, SRC>(a, copies, grid_y, stream)
-                : launch<TQ_FMT_NV4, 16, SRC>(a, copies, grid_y, stream);
-    default: break;
+    case 8: return launch_format<8>(format, a, copies, grid_y, stream);
+    case 16: return launch_format<16>(format, a, copies, grid_y, stream);
+    case 32: return launch_format<32>(format, a, copies, grid_y, stream);
+    default: return launch_format<64>(format, a, copies, grid_y, stream);
   }
-  if constexpr (SRC == kBf16) {
-    if (nt == 32)
-      return mx ? launch<TQ_FMT_MX4, 32, SRC>(a, copies, grid_y, stream)
-                : launch<TQ_FMT_NV4, 32, SRC>(a, copies, grid_y, stream);
-    return mx ? launch<TQ_FMT_MX4, 64, SRC>(a, copies, grid_y, stream)
-              : launch<TQ_FMT_NV4, 64, SRC>(a, copies, grid_y, stream);
-  }
-  return cudaErrorInvalidValue;
 }
 
 int rows_per_pass(int64_t rows) {
@@ -792,6 +740,12 @@ RowArgs weight_args(const WeightsView &w) {
 cudaError_t linear_f4_bf16(const WeightsView &w, const __nv_bfloat16 *x,
                            int64_t batch, int64_t ldx, float *y, int64_t ldy,
                            cudaStream_t stream) {
+  // Up to 3 (MX4: 4) rows the digits of x cost less than decoding the weights:
+  // 21504 x 5376 (MX4) at 1, 2, 4, 8 rows 16.5, 18, 23, 36 us there against
+  // 25, 26, 27, 29 us here; 5376 x 21504 (NV4) at 1, 2, 4 rows 18.7, 22, 28
+  // against 24, 24.5, 25.6 us.
+  if (batch <= (w.format == TQ_FMT_MX4 ? 4 : 3) && decode_f4_supported(w, 1))
+    return decode_f4_bf16(w, x, batch, ldx, y, ldy, stream);
   RowArgs a = weight_args(w);
   a.x = x;
   a.ldx = ldx;
@@ -808,7 +762,7 @@ cudaError_t linear_f4_bf16(const WeightsView &w, const __nv_bfloat16 *x,
     b.x += p * nt * ldx;
     b.y = y + p * nt * ldy;
     b.batch -= p * nt;
-    e = launch_nt<kBf16>(w.format, nt, b, now, now, stream);
+    e = launch_nt(w.format, nt, b, now, now, stream);
   }
   return e;
 }
@@ -818,6 +772,11 @@ cudaError_t launch_linear_experts_f4(const WeightsView &w, int n_experts,
                                      const __nv_bfloat16 *x, int64_t ldx,
                                      float *y, int64_t ldy, int32_t *status,
                                      cudaStream_t stream) {
+  // The same trade: 64 rows over 128 experts of 768 x 2048 (MX4) 22 us there
+  // against 25 us here, 500 rows (NV4) 66 against 46 us.
+  if (tokens <= n_experts && decode_f4_supported(w, n_experts))
+    return decode_f4_experts(w, n_experts, ids, tokens, x, ldx, y, ldy, status,
+                             stream);
   RowArgs a = weight_args(w);
   a.x = x;
   a.ldx = ldx;
@@ -830,22 +789,7 @@ cudaError_t launch_linear_experts_f4(const WeightsView &w, int n_experts,
   // experts that get rows at all, and the rows of one
   const int64_t used = tokens < n_experts ? tokens : n_experts;
   const int nt = rows_per_pass(2 * ((tokens + n_experts - 1) / n_experts));
-  return launch_nt<kBf16>(w.format, nt, a, used, n_experts, stream);
-}
-
-bool rows_f4_packed_supported(const WeightsView &x) { return x.n <= 16; }
-
-cudaError_t rows_f4_packed(const WeightsView &w, const WeightsView &x, void *y,
-                           int64_t ldy, int y_type, cudaStream_t stream) {
-  RowArgs a = weight_args(w);
-  a.xcodes = x.codes;
-  a.xscales = reinterpret_cast<const uint8_t *>(x.scales);
-  a.xg = x.lut;
-  a.batch = x.n;
-  a.y = y;
-  a.ldy = ldy;
-  a.y_bf16 = y_type == TQ_Y_BF16;
-  return launch_nt<kPacked>(w.format, rows_per_pass(x.n), a, 1, 1, stream);
+  return launch_nt(w.format, nt, a, used, n_experts, stream);
 }
 
 }  // namespace tq
