@@ -284,6 +284,19 @@ tq_status tq_unpack(const tq_weights *w, void *W_bf16_out, int32_t *dev_status,
 tq_status tq_linear(const tq_weights *w, const void *x_bf16, int64_t batch,
                     int64_t ldx, float *y, int64_t ldy, void *cuda_stream);
 
+/* tq_linear with scratch memory of the caller: 4-bit weights and larger
+ * batches run on the block-scaled tensor cores, with x written there as 4-bit
+ * digits first (same accuracy). tq_linear_workspace says how many bytes help
+ * (0: none do, or invalid arguments; host only).
+ *   workspace  device, 256-byte aligned, workspace_bytes long, or NULL; with
+ *              NULL or too few bytes the call is tq_linear. Its contents are
+ *              undefined afterwards; calls that share one must be ordered (on
+ *              one stream they are). */
+size_t tq_linear_workspace(const tq_weights *w, int64_t batch);
+tq_status tq_linear_ws(const tq_weights *w, const void *x_bf16, int64_t batch,
+                       int64_t ldx, float *y, int64_t ldy, void *workspace,
+                       size_t workspace_bytes, void *cuda_stream);
+
 /* Expert-indexed Format A weights (FUCINA README, "The method": hot experts
  * carry both ternary planes W ~ d1 T1 + d2 T2, cold experts one; the experts
  * are stored hot-first, so the second plane covers the prefix 0 .. n_hot - 1).

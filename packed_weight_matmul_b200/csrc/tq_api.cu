@@ -223,21 +223,41 @@ tq_status tq_encode_b(const void *W_bf16, int64_t n, int64_t k,
       alpha_out, dev_status, static_cast<cudaStream_t>(cuda_stream)));
 }
 
+size_t tq_linear_workspace(const tq_weights *w, int64_t batch) {
+  tq::WeightsView v;
+  if (check_weights(w, &v) != TQ_OK || batch < 1) return 0;
+  if (!tq::is_f4(v.format) || v.n == 0 || v.k == 0) return 0;
+  return (size_t)tq::digits_f4_workspace(v, batch);
+}
+
 tq_status tq_linear(const tq_weights *w, const void *x_bf16, int64_t batch,
                     int64_t ldx, float *y, int64_t ldy, void *cuda_stream) {
+  return tq_linear_ws(w, x_bf16, batch, ldx, y, ldy, nullptr, 0, cuda_stream);
+}
+
+tq_status tq_linear_ws(const tq_weights *w, const void *x_bf16, int64_t batch,
+                       int64_t ldx, float *y, int64_t ldy, void *workspace,
+                       size_t workspace_bytes, void *cuda_stream) {
   tq::WeightsView v;
   const tq_status st = check_weights(w, &v);
   if (st != TQ_OK) return st;
   if (x_bf16 == nullptr || y == nullptr || batch < 1) return TQ_ERR_INVALID_ARG;
   if (ldx < v.k || ldy < v.n) return TQ_ERR_SHAPE;
   if (!aligned(x_bf16, 16) || ldx % 8 != 0) return TQ_ERR_ALIGNMENT;
-  if (!aligned(y, 4)) return TQ_ERR_ALIGNMENT;
+  if (!aligned(y, 4) || !aligned(workspace, 256)) return TQ_ERR_ALIGNMENT;
   if (v.n == 0) return TQ_OK;
   cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
   if (v.k == 0) {  // empty sum: y = 0
     return from_cuda(cudaMemset2DAsync(y, (size_t)ldy * sizeof(float), 0,
                                        (size_t)v.n * sizeof(float),
                                        (size_t)batch, stream));
+  }
+  if (workspace != nullptr && tq::is_f4(v.format)) {
+    const int64_t need = tq::digits_f4_workspace(v, batch);
+    if (need > 0 && (uint64_t)need <= workspace_bytes)
+      return from_cuda(tq::digits_f4(
+          v, static_cast<const __nv_bfloat16 *>(x_bf16), batch, ldx, y, ldy,
+          static_cast<uint8_t *>(workspace), stream));
   }
   return from_cuda(tq::launch_linear(
       v, static_cast<const __nv_bfloat16 *>(x_bf16), batch, ldx, y, ldy,

@@ -8,21 +8,8 @@
 // multiplies them by a 4-bit x. Packed x (tq_linear_f4) is such a matrix
 // already. A bf16 x is written as a sum of 8 of them, exactly enough:
 //
-//   In a block of x let f be the exponent of its largest magnitude and
-//   r = x 2^(1 - f) in (-4, 4). Digits in base 8: d_i = round(r_i) in
-//   {-4 .. 4}, r_{i+1} = 8 (r_i - d_i), so x = 2^(f - 1) sum_i d_i 8^-i, and
-//   after 8 digits the rest is at most 2^-23 of the block's largest value.
-//   All of -4 .. 4 are E2M1 values. Row 8 b + i of the B operand holds d_i of
-//   row b of x.
-//   MX4: its block scale 2^(f - X - 1 - 3 i) is an E8M0 byte, X the exponent
-//        of the largest value of the row in this CTA's slice of K.
-//   NV4: an E4M3 byte reaches from 2^-9 to 2^8 only, so row i has a factor
-//        2^(X - 9 - 3 i) of its own, applied to its sum, and the block scale
-//        2^(f - X + 8); blocks below 2^-17 of the row's largest take the
-//        smallest scale, which leaves them off by 2^-40 of it.
-//   y = 2^X sum_i D_i (MX4) or 2^(X - 9) sum_i 8^-i D_i (NV4), D the fp32
-//   accumulators. NaN and Inf count as 0 in the digits; their rows of x are
-//   flagged and the products with them added to the sums afterwards.
+//   (tq_f4_digits.cuh: base-8 digits, row 8 b + i of the B operand holds digit
+//   i of row b of x).
 //
 // Bound by the codes' way from HBM: an MMA of 64 k takes 41 to 64 cycles for
 // 8192 weights, 2 to 3 times the rate at which HBM delivers them. A digit
@@ -40,6 +27,7 @@
 // Every wait is bounded; one that gives up leaves NaN in the CTA's outputs.
 #include <cooperative_groups.h>
 
+#include "tq_f4_digits.cuh"
 #include "tq_f4_tc.cuh"
 
 namespace tq {
@@ -103,62 +91,6 @@ struct DecodeArgs {
   int32_t *status;
 };
 
-__device__ __forceinline__ uint32_t max_mag8(const uint4 &w) {
-  const uint32_t m = __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
-                              __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
-  return max(m >> 16, m & 0xFFFFu);
-}
-
-// NaN and Inf become 0.
-__device__ __noinline__ uint4 only_finite8(uint4 w) {
-  uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if ((v[i] & 0x7F80u) == 0x7F80u) v[i] &= 0xFFFF0000u;
-    if ((v[i] & 0x7F800000u) == 0x7F800000u) v[i] &= 0x0000FFFFu;
-  }
-  return make_uint4(v[0], v[1], v[2], v[3]);
-}
-
-struct F2 {
-  uint64_t v;
-};
-__device__ __forceinline__ F2 pack2(float a, float b) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(r.v)
-      : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
-// E2M1 codes of 8 small integers, the first lowest.
-__device__ __forceinline__ uint32_t codes8(const F2 (&q)[4]) {
-  uint32_t r;
-  asm("{\n .reg .b8 t0, t1, t2, t3;\n .reg .f32 a, b;\n"
-      " mov.b64 {a, b}, %1;\n cvt.rn.satfinite.e2m1x2.f32 t0, b, a;\n"
-      " mov.b64 {a, b}, %2;\n cvt.rn.satfinite.e2m1x2.f32 t1, b, a;\n"
-      " mov.b64 {a, b}, %3;\n cvt.rn.satfinite.e2m1x2.f32 t2, b, a;\n"
-      " mov.b64 {a, b}, %4;\n cvt.rn.satfinite.e2m1x2.f32 t3, b, a;\n"
-      " mov.b32 %0, {t0, t1, t2, t3};\n}"
-      : "=r"(r)
-      : "l"(q[0].v), "l"(q[1].v), "l"(q[2].v), "l"(q[3].v));
-  return r;
-}
-
 __device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n)
                : "memory");
@@ -166,20 +98,6 @@ __device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
 
 __device__ __forceinline__ void fence_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
-// One weight, for the rows of x that hold NaN or Inf.
-template <int FMT>
-__device__ float one_weight(const uint8_t *codes, const uint8_t *scales,
-                            int64_t row, int64_t k_cols, int k) {
-  const uint32_t b = codes[row * (k_cols / 2) + k / 2] >> (4 * (k & 1));
-  const uint32_t m = b & 7u;
-  const float mag =
-      m < 2 ? 0.5f * m
-            : __uint_as_float(((m >> 1) + 126u) << 23 | (m & 1u) << 22);
-  const float s = f4_scale<FMT>(
-      scales[row * (k_cols / f4_block(FMT)) + k / f4_block(FMT)]);
-  return (b & 8u ? -mag : mag) * s;
 }
 
 template <int FMT, int NT, int SRC>
@@ -506,17 +424,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
             if (FMT == TQ_FMT_MX4)
               m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-            const int X = s_exp[r], f = max((int)(m >> 7), 1);
-            uint32_t byte, scale;  // block scale; exponent field of 1 / (2^..)
-            if (FMT == TQ_FMT_MX4) {
-              const int b = max(126 + f - X, 0);
-              byte = (uint32_t)b;
-              scale = (uint32_t)(381 - X - b);
-            } else {
-              const int e = max(f - X + 8, -9);
-              byte = e >= -6 ? (uint32_t)(e + 7) << 3 : 1u << (e + 9);
-              scale = (uint32_t)(263 - X - e);
-            }
+            uint32_t byte, field;
+            digit_scale<FMT>(max((int)(m >> 7), 1), s_exp[r], &byte, &field);
             constexpr int kLanes = f4_block(FMT) / 8;
             if (lane % kLanes == 0)
               asm volatile("st.shared.u8 [%0], %1;" ::"r"(
@@ -524,33 +433,15 @@ __global__ void __launch_bounds__(kThreads, 2)
                                lane / kLanes),
                            "r"(byte)
                            : "memory");
-            const float f0 = __uint_as_float(scale << 23);
-            const F2 f2 = pack2(f0, f0);
-            F2 q[4], v[4];
-            const uint32_t h[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              v[e] = mul2(pack2(__uint_as_float(h[e] << 16),
-                                __uint_as_float(h[e] & 0xFFFF0000u)),
-                          f2);
             // row 8 r + i: 16-byte chunk c (32 codes) lies at c ^ i
             const uint32_t at =
                 base + P::kOffB + s * P::kB + r * 1024 + (lane & 3) * 4;
-            const F2 magic = pack2(12582912.0f, 12582912.0f);  // 1.5 2^23
-            const F2 minus = pack2(-12582912.0f, -12582912.0f);
-            const F2 neg = pack2(-1.0f, -1.0f), eight = pack2(8.0f, 8.0f);
-#pragma unroll
-            for (int d = 0; d < 8; ++d) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                q[e] = add2(add2(v[e], magic), minus);  // nearest integer
-                v[e] = mul2(fma2(q[e], neg, v[e]), eight);
-              }
+            digits8(w, field, [&](int d, uint32_t codes) {
               asm volatile("st.shared.b32 [%0], %1;" ::"r"(
                                at + d * 128 + (((lane >> 2) ^ d) << 4)),
-                           "r"(codes8(q))
+                           "r"(codes)
                            : "memory");
-            }
+            });
           }
           fence_async();
           __syncwarp();
@@ -580,23 +471,10 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int h = 0; h < 2; ++h) {
               const int b = c / 8 + h;
               if (b >= rows) break;
-              float t = __uint_as_float(v[8 * h + 7]);
-#pragma unroll
-              for (int d = 6; d >= 0; --d)  // the smallest digits first
-                t = FMT == TQ_FMT_MX4
-                        ? t + __uint_as_float(v[8 * h + d])
-                        : fmaf(t, 0.125f, __uint_as_float(v[8 * h + d]));
-              t = scalbnf(t, s_exp[b] - (FMT == TQ_FMT_MX4 ? 127 : 136));
-              if (s_odd[b] && row0 + r < a.n) {
-                // add the products with NaN and Inf
-                const __nv_bfloat16 *p = x_row(b);
-                for (int k = (int)k0; k < (int)k1; ++k) {
-                  const float xv = __bfloat162float(p[k]);
-                  if (!(fabsf(xv) < __int_as_float(0x7F800000)))
-                    t += xv * one_weight<FMT>(a.codes, a.wscales, wrow + r,
-                                              a.k, k);
-                }
-              }
+              float t = digit_sum<FMT>(&v[8 * h], s_exp[b]);
+              if (s_odd[b] && row0 + r < a.n)
+                t += odd_products<FMT>(x_row(b), (int)k0, (int)k1, a.codes,
+                                       a.wscales, wrow + r, a.k);
               part[b * P::kPitch + r] = ok ? t : __int_as_float(0x7FC00000);
             }
           }

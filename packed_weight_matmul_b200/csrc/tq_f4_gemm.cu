@@ -31,6 +31,7 @@
 //
 // Every wait is bounded; one that gives up leaves NaN in the outputs of the
 // tiles that were not finished.
+#include "tq_f4_digits.cuh"
 #include "tq_f4_tc.cuh"
 
 namespace tq {
@@ -87,6 +88,12 @@ struct Args {
   void *y;
   int64_t n, batch, ldy;
   int k, tiles_m, tiles_n, y_bf16;
+  // Digits: every 8 batch rows are the digits of one row of x (tq_f4_digits.cuh)
+  // of exponent exps[b]; null otherwise. odd[b]: x holds NaN or Inf there.
+  const int *exps, *odd;
+  const __nv_bfloat16 *x;
+  int64_t ldx;
+  const uint8_t *wcodes;
 };
 
 template <int CG>
@@ -425,7 +432,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       // tile can start while they are stored: all of them as bf16 pairs (two
       // columns of this lane's row), 64 in fp32.
       uint32_t h[kCols / 2 < 16 ? 16 : kCols / 2] = {};
-      if (args.y_bf16) {
+      if (args.exps != nullptr) {
+#pragma unroll 1
+        for (int c = 0; c < cols; c += 16) {
+          uint32_t v[16];
+          tmem_ld16(src + c, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int64_t b = (b0 + c) / 8 + j;
+            if (c + 8 * j >= cols) break;
+            float f = digit_sum<FMT>(&v[8 * j], __ldg(args.exps + b)) * gn;
+            if (row < args.n) {
+              if (__ldg(args.odd + b))
+                f += g * odd_products<FMT>(args.x + b * args.ldx, 0, args.k,
+                                           args.wcodes, args.wscales, row,
+                                           args.k);
+              static_cast<float *>(args.y)[b * args.ldy + row] = f;
+            }
+          }
+          __syncwarp();
+        }
+        drained();
+      } else if (args.y_bf16) {
 #pragma unroll
         for (int c = 0; c < kCols; c += 16) {
           if (c >= cols) break;
@@ -506,8 +535,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int FMT, int NT, int CG>
-cudaError_t launch(const WeightsView &w, const WeightsView &x, void *y,
-                   int64_t ldy, int y_type, cudaStream_t stream) {
+cudaError_t launch(const WeightsView &w, const WeightsView &x, Args a,
+                   cudaStream_t stream) {
   using P = Plan<FMT, NT, CG>;
   int dev = 0, sms = 148;
   cudaError_t e = cudaGetDevice(&dev);
@@ -516,19 +545,8 @@ cudaError_t launch(const WeightsView &w, const WeightsView &x, void *y,
   CUtensorMap mw, mx;
   if ((e = code_map(&mw, w, kRowsM)) != cudaSuccess) return e;
   if ((e = code_map(&mx, x, NT / CG)) != cudaSuccess) return e;
-  Args a = {};
-  a.wscales = reinterpret_cast<const uint8_t *>(w.scales);
-  a.xscales = reinterpret_cast<const uint8_t *>(x.scales);
-  a.wg = w.lut;
-  a.xg = x.lut;
-  a.y = y;
-  a.n = w.n;
-  a.batch = x.n;
-  a.ldy = ldy;
-  a.k = (int)w.k;
   a.tiles_m = (int)((w.n + CG * kRowsM - 1) / (CG * kRowsM));
   a.tiles_n = (int)((x.n + NT - 1) / NT);
-  a.y_bf16 = y_type == TQ_Y_BF16;
   const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
   const int groups = (int)(tiles < sms / CG ? tiles : sms / CG);
   auto kern = product_f4_kernel<FMT, NT, CG>;
@@ -553,10 +571,10 @@ cudaError_t launch(const WeightsView &w, const WeightsView &x, void *y,
 }
 
 template <int FMT>
-cudaError_t dispatch(const WeightsView &w, const WeightsView &x, void *y,
-                     int64_t ldy, int y_type, cudaStream_t stream) {
-  if (x.n <= 32) return launch<FMT, 32, 1>(w, x, y, ldy, y_type, stream);
-  if (x.n <= 64) return launch<FMT, 64, 1>(w, x, y, ldy, y_type, stream);
+cudaError_t dispatch(const WeightsView &w, const WeightsView &x, const Args &a,
+                     cudaStream_t stream) {
+  if (x.n <= 32) return launch<FMT, 32, 1>(w, x, a, stream);
+  if (x.n <= 64) return launch<FMT, 64, 1>(w, x, a, stream);
   // A wave of 256 x 256 tiles takes 7/5 of the time of a wave of 128 x 128
   // tiles, two of which cover half of it (measured per 32 stages on 148 SMs:
   // 14.1 and 10.1 us), so the large tile wins where its waves are full: 98
@@ -571,8 +589,23 @@ cudaError_t dispatch(const WeightsView &w, const WeightsView &x, void *y,
     return (tiles + at_once - 1) / at_once;
   };
   if (x.n > 128 && 7 * waves(256, 256, sms / 2) <= 5 * waves(128, 128, sms))
-    return launch<FMT, 256, 2>(w, x, y, ldy, y_type, stream);
-  return launch<FMT, 128, 1>(w, x, y, ldy, y_type, stream);
+    return launch<FMT, 256, 2>(w, x, a, stream);
+  return launch<FMT, 128, 1>(w, x, a, stream);
+}
+
+Args args_of(const WeightsView &w, const WeightsView &x, void *y, int64_t ldy) {
+  Args a = {};
+  a.wscales = reinterpret_cast<const uint8_t *>(w.scales);
+  a.xscales = reinterpret_cast<const uint8_t *>(x.scales);
+  a.wg = w.lut;
+  a.xg = x.lut;
+  a.y = y;
+  a.n = w.n;
+  a.batch = x.n;
+  a.ldy = ldy;
+  a.k = (int)w.k;
+  a.wcodes = w.codes;
+  return a;
 }
 
 }  // namespace
@@ -582,9 +615,23 @@ cudaError_t launch_linear_f4(const WeightsView &w, const WeightsView &x,
                              cudaStream_t stream) {
   if (x.n <= 64 && decode_f4_supported(w, 1))
     return decode_f4_packed(w, x, y, ldy, y_type, stream);
-  return w.format == TQ_FMT_MX4
-             ? dispatch<TQ_FMT_MX4>(w, x, y, ldy, y_type, stream)
-             : dispatch<TQ_FMT_NV4>(w, x, y, ldy, y_type, stream);
+  Args a = args_of(w, x, y, ldy);
+  a.y_bf16 = y_type == TQ_Y_BF16;
+  return w.format == TQ_FMT_MX4 ? dispatch<TQ_FMT_MX4>(w, x, a, stream)
+                                : dispatch<TQ_FMT_NV4>(w, x, a, stream);
+}
+
+cudaError_t product_f4_digits(const WeightsView &w, const WeightsView &u,
+                              const int *exps, const int *odd,
+                              const __nv_bfloat16 *x, int64_t ldx, float *y,
+                              int64_t ldy, cudaStream_t stream) {
+  Args a = args_of(w, u, y, ldy);
+  a.exps = exps;
+  a.odd = odd;
+  a.x = x;
+  a.ldx = ldx;
+  return w.format == TQ_FMT_MX4 ? dispatch<TQ_FMT_MX4>(w, u, a, stream)
+                                : dispatch<TQ_FMT_NV4>(w, u, a, stream);
 }
 
 }  // namespace tq

@@ -61,8 +61,8 @@ template <int FMT, int NT>
 struct RowPlan {
   static constexpr int kWarps = 8, kThreads = 32 * kWarps;
   static constexpr int kTile = 16 * kWarps;  // weight rows of a CTA
-  static constexpr int kCtas = NT <= 16 ? 3 : 2;  // per SM
-  static constexpr int kRing = NT <= 16 ? 2 : 3;  // stages of a warp's ring
+  static constexpr int kCtas = 2;  // per SM
+  static constexpr int kRing = 3;  // stages of a warp's ring
   // buffers of x: with 64 rows there is room for one only
   static constexpr int kXBufs = NT == 64 ? 1 : 2;
   static constexpr int kScaleRow = FMT == TQ_FMT_MX4 ? 8 : 16;  // per stage

@@ -7,6 +7,7 @@ libtq.so and raises TqError if it has not been built: there is no fallback.
 Device tensors are passed by pointer; the CUDA stream defaults to torch's
 current stream. A non-TQ_OK status raises TqError (status in `.status`).
 """
+import contextlib
 import ctypes as C
 import os
 
@@ -30,7 +31,8 @@ ENTRY_POINTS = ("tq_packed_bytes", "tq_build_lut", "tq_quantize_pack",
                 "tq_testing_force_linear_path", "tq_testing_tc_self_check",
                 "tq_testing_tc_trace", "tq_linear_experts", "tq_pack7",
                 "tq_build_lut7", "tq_testing_tc_split", "tq_quantize_f4",
-                "tq_linear_f4", "tq_linear_experts_f4")
+                "tq_linear_f4", "tq_linear_experts_f4",
+                "tq_linear_workspace", "tq_linear_ws")
 
 
 class TqError(RuntimeError):
@@ -98,6 +100,11 @@ def _load():
                                     i64, P, P]
     L.tq_quantize_f4.restype = C.c_int
     L.tq_quantize_f4.argtypes = [P, i64, i64, i64, i32, P, P, P, i32, P, P]
+    L.tq_linear_workspace.restype = C.c_size_t
+    L.tq_linear_workspace.argtypes = [C.POINTER(tq_weights), i64]
+    L.tq_linear_ws.restype = C.c_int
+    L.tq_linear_ws.argtypes = [C.POINTER(tq_weights), P, i64, i64, P, i64, P,
+                               C.c_size_t, P]
     L.tq_linear_f4.restype = C.c_int
     L.tq_linear_f4.argtypes = [C.POINTER(tq_weights), C.POINTER(tq_weights),
                                P, i64, i32, P]
@@ -130,6 +137,17 @@ def _stream(stream):
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return stream
+
+
+def _torch_stream(stream):
+    """Context in which `stream` (as the calls take it) is torch's current
+    stream."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream) if stream else \
+            torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 def _check(status, what):
@@ -391,8 +409,19 @@ def tq_linear(w: Weights, x, y, batch=None, ldx=None, ldy=None, stream=None,
         ldx = x.stride(0) if x.dim() == 2 else w.k
     if ldy is None:
         ldy = y.stride(0) if y.dim() == 2 else w.n
-    st = _lib.tq_linear(C.byref(w.desc), _ptr(x), batch, ldx, _ptr(y), ldy,
-                        _stream(stream))
+    need = 0
+    if w.desc.format in F4_BLOCK:
+        need = _lib.tq_linear_workspace(C.byref(w.desc), batch)
+    if need:
+        # scratch from torch's allocator, on the stream that uses it
+        with _torch_stream(stream):
+            ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+            st = _lib.tq_linear_ws(C.byref(w.desc), _ptr(x), batch, ldx,
+                                   _ptr(y), ldy, ws.data_ptr(), need,
+                                   _stream(None))
+    else:
+        st = _lib.tq_linear(C.byref(w.desc), _ptr(x), batch, ldx, _ptr(y), ldy,
+                            _stream(stream))
     if check:
         _check(st, "tq_linear")
     return st
