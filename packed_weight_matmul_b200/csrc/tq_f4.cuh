@@ -86,9 +86,12 @@ cudaError_t decode_f4_experts(const WeightsView &w, int n_experts,
                               const __nv_bfloat16 *x, int64_t ldx, float *y,
                               int64_t ldy, int32_t *status,
                               cudaStream_t stream);
+namespace f4 {
+struct DigitArgs;
+}
 cudaError_t decode_f4_packed(const WeightsView &w, const WeightsView &x,
                              void *y, int64_t ldy, int y_type,
-                             cudaStream_t stream);
+                             const f4::DigitArgs &digits, cudaStream_t stream);
 
 
 // tq_linear with a workspace (tq_f4_digits.cu): bytes (0: of no use), call.
@@ -96,10 +99,9 @@ int64_t digits_f4_workspace(const WeightsView &w, int64_t batch);
 cudaError_t digits_f4(const WeightsView &w, const __nv_bfloat16 *x,
                       int64_t batch, int64_t ldx, float *y, int64_t ldy,
                       uint8_t *workspace, cudaStream_t stream);
-// The product with the digit rows `u` of x (tq_f4_gemm.cu).
-cudaError_t product_f4_digits(const WeightsView &w, const WeightsView &u,
-                              const int *exps, const int *odd,
-                              const __nv_bfloat16 *x, int64_t ldx, float *y,
-                              int64_t ldy, cudaStream_t stream);
+// The product with packed rows of x, which may be digits (tq_f4_gemm.cu).
+cudaError_t product_f4(const WeightsView &w, const WeightsView &x, void *y,
+                       int64_t ldy, int y_type, const f4::DigitArgs &digits,
+                       cudaStream_t stream);
 
 }  // namespace tq

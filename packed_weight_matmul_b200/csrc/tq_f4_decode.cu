@@ -21,7 +21,8 @@
 // adds them in rank order through distributed shared memory. 14 warps:
 //   warp 0       TMA producer (codes; packed x); tensor-memory allocation
 //   warp 1       MMA issuer
-//   warps 2-5    scales to tensor memory, as in tq_f4_gemm.cu
+//   warps 2-5    scales to tensor memory, as in tq_f4_gemm.cu (packed x: and
+//                warps 6-9, in turn)
 //   warps 6-13   bf16 x: exponents, digits into the swizzled B tiles; the first
 //                four read the accumulator at the end
 // Every wait is bounded; one that gives up leaves NaN in the CTA's outputs.
@@ -54,26 +55,32 @@ struct DecodePlan {
   static constexpr uint32_t kA = kTile * kF4StageRow;
   static constexpr uint32_t kB = NT * kF4StageRow;
   static constexpr uint32_t kPiece = kWords * 4;  // scale bytes of a stage
-  static constexpr int kUnitStages = 4;
+  // Packed x leaves warps free: a second group of four moves scales, and they
+  // take turns by units of 2 stages. A wait by parity is right one phase
+  // ahead, so the ring has to be longer than the other group's unit.
+  static constexpr int kGroups = SRC == kPacked ? 2 : 1;
+  static constexpr int kUnitStages = SRC == kPacked ? 2 : 4;
   static constexpr uint32_t kUnit = kUnitStages * kPiece;
   static constexpr int kScaleRows = kTile + (SRC == kPacked ? NT : 0);
-  static constexpr uint32_t kScales = kScaleRows * kUnit;
+  static constexpr uint32_t kScales = kScaleRows * kUnit;  // of one group
   static constexpr uint32_t kExp = SRC == kBf16 ? kRows * 16 : 0;
-  static constexpr uint32_t kFixed = 2048 + kScales +
+  static constexpr uint32_t kFixed = 2048 + kGroups * kScales +
                                      (SRC == kBf16 ? kSegment * 4 + 1024 : 0);
   static constexpr int kFit = (int)((kSmemLimit - kFixed) / (kA + kB + kExp));
   static constexpr int kFitT = (int)((kColumns - NT) / kScaleCols);
   static constexpr int kStages0 = kFit < kFitT ? kFit : kFitT;
   static constexpr int kStages = kStages0 < 8 ? kStages0 : 8;
-  static_assert(kStages >= 3, "ring too short");
+  static_assert(kStages >= 3 && (kGroups == 1 || kStages > kUnitStages),
+                "ring too short");
   static constexpr uint32_t kOffB = kStages * kA;
   static constexpr uint32_t kOffS = kOffB + kStages * kB;
-  static constexpr uint32_t kOffE = kOffS + kScales;
+  static constexpr uint32_t kOffE = kOffS + kGroups * kScales;
   static constexpr uint32_t kOffBar = kOffE + kStages * kExp;
   static constexpr uint32_t kSmem = kOffBar + 256 + 1024;
   static constexpr int kPitch = kTile + 4;  // of the partial tile
   static_assert(kRows * kPitch * 4 <= kOffS, "partial tile");
-  static constexpr int kStaged = kRows > 8 ? kRows / 8 : 1;  // per warp
+  static constexpr int kStaged = SRC == kBf16 && kRows > 8 ? 2 : 1;  // per warp
+  static_assert(SRC == kPacked || kRows <= 16, "rows per warp");
 };
 
 struct DecodeArgs {
@@ -83,6 +90,7 @@ struct DecodeArgs {
   int64_t ldx;
   const uint8_t *xscales;  // packed
   const float *xg;
+  DigitArgs digits;  // packed
   void *y;
   int64_t n, batch, ldy;
   int k, y_bf16, ks;
@@ -151,6 +159,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   int64_t expert = a.ids != nullptr ? blockIdx.y : 0;
   uint32_t done = 0;  // stages of the passes before
 
+  // packed rows that make one row of y
+  const int per = SRC == kPacked && a.digits.exps != nullptr ? 8 : 1;
   // `rows` rows of x (s_rows[first + i], or b0 + i): one pass over K
   auto pass = [&](int pass_no, int first, int64_t b0, int rows) {
     const int64_t wrow = expert * a.n + row0;  // first weight row
@@ -159,57 +169,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     // warp skips S stages at most.
     const int per_stage = rows <= 1 ? 1 : rows <= 2 ? 2 : rows <= 4 ? 4 : 8;
     const int at_once = 8 / per_stage < S ? 8 / per_stage : S;
-    if (warp == 0) {
-      if (lane == 0) {
-        bool ok = true;
-        int i = 0;
-        for (; i < steps; ++i) {
-          const uint32_t it = done + i, s = it % S, ph = (it / S) & 1u;
-          ok = mbar_wait(empty + 8 * s, ph ^ 1u, abort_addr, kWaitLimitNs);
-          if (!ok) break;
-          mbar_arrive_expect_tx(ready + 8 * s,
-                                P::kA + (SRC == kPacked ? P::kB : 0u));
-          tma_load_2d(base + s * P::kA, &tmap_w,
-                      (st0 + i) * (int)kF4StageRow, (int)wrow, ready + 8 * s);
-          if (SRC == kPacked)
-            tma_load_2d(base + P::kOffB + s * P::kB, &tmap_x,
-                        (st0 + i) * (int)kF4StageRow, (int)b0, ready + 8 * s);
-        }
-        // every copy issued has landed, and every MMA that read one is done
-        for (int j = i > S ? i - S : 0; j < i; ++j)
-          mbar_wait(empty + 8 * ((done + j) % S), ((done + j) / S) & 1u);
-      }
-    } else if (warp == 1) {
-      bool ok = true, here = false;
-      int i = 0;
-      for (; i < steps; ++i) {  // the whole warp, see mma_stage
-        const uint32_t it = done + i, s = it % S, ph = (it / S) & 1u;
-        if (!here) {
-          ok = mbar_wait(ready + 8 * s, ph, abort_addr, kWaitLimitNs);
-          ok = __all_sync(0xFFFFFFFFu, ok);
-          if (!ok) break;
-        }
-        tc_fence_after_sync();
-        const bool next =
-            mbar_test<1>(ready + 8 * ((it + 1) % S), ((it + 1) / S) & 1u);
-        const uint32_t sa = tmem_scales + s * P::kScaleCols;
-        mma_stage<FMT, 1>(
-            tmem, smem_desc_kmajor_sw128(base + s * P::kA),
-            smem_desc_kmajor_sw128(base + P::kOffB + s * P::kB),
-            idesc_f4<FMT>(kTile, NT, 0u),
-            idesc_f4<FMT>(kTile, NT, FMT == TQ_FMT_MX4 ? 2u : 0u), sa,
-            sa + P::kWords * 4, P::kBCols, i != 0 ? 1u : 0u, empty + 8 * s);
-        here = __all_sync(0xFFFFFFFFu, next);
-      }
-      if (ok) commit<1>(dfull);
-      for (int j = i > S ? i - S : 0; j < i; ++j)
-        mbar_wait(empty + 8 * ((done + j) % S), ((done + j) / S) & 1u);
-    } else if (warp < 6) {
-      const int at = tid - 64;
+    // Scales to tensor memory: group `turn` of four warps.
+    auto move_scales = [&](int turn) {
+      const int at = (tid - 64) & 127;
       const uint32_t quarter = (uint32_t)(warp & 3) << 21;
       const int row_bytes = a.k / f4_block(FMT);
       const bool whole = a.k % kStageK == 0;
-      const uint32_t buf = base + P::kOffS;
+      const uint32_t buf = base + P::kOffS + turn * P::kScales;
       constexpr int kPieces = P::kUnitStages, kPass = 128 / kPieces;
       constexpr int kPieceWords = (int)P::kPiece / 4;
       constexpr int kLoads = (P::kScaleRows + kPass - 1) / kPass;
@@ -244,11 +210,11 @@ __global__ void __launch_bounds__(kThreads, 2)
           });
       };
       const int units = (steps + P::kUnitStages - 1) / P::kUnitStages;
-      if (units > 0) load(0);
+      if (turn < units) load(turn);
       bool ok = true;
 #pragma unroll 1
-      for (int u = 0; u < units; ++u) {
-        bar_sync(1, 128);  // the last unit has been read
+      for (int u = turn; u < units; u += P::kGroups) {
+        bar_sync(1 + 2 * turn, 128);  // the last unit has been read
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
           if (FMT == TQ_FMT_NV4) {  // E4M3 scales are read without their sign
@@ -260,8 +226,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                                                            my_piece),
                         v[j]);
         }
-        bar_sync(1, 128);
-        if (u + 1 < units) load(u + 1);
+        bar_sync(1 + 2 * turn, 128);
+        if (u + P::kGroups < units) load(u + P::kGroups);
         const int left = steps - u * P::kUnitStages;
 #pragma unroll 1
         for (int i = 0; i < left && i < P::kUnitStages; ++i) {
@@ -322,7 +288,57 @@ __global__ void __launch_bounds__(kThreads, 2)
           __syncwarp();
         }
       }
+    };
+
+    if (warp == 0) {
+      if (lane == 0) {
+        bool ok = true;
+        int i = 0;
+        for (; i < steps; ++i) {
+          const uint32_t it = done + i, s = it % S, ph = (it / S) & 1u;
+          ok = mbar_wait(empty + 8 * s, ph ^ 1u, abort_addr, kWaitLimitNs);
+          if (!ok) break;
+          mbar_arrive_expect_tx(ready + 8 * s,
+                                P::kA + (SRC == kPacked ? P::kB : 0u));
+          tma_load_2d(base + s * P::kA, &tmap_w,
+                      (st0 + i) * (int)kF4StageRow, (int)wrow, ready + 8 * s);
+          if (SRC == kPacked)
+            tma_load_2d(base + P::kOffB + s * P::kB, &tmap_x,
+                        (st0 + i) * (int)kF4StageRow, (int)b0, ready + 8 * s);
+        }
+        // every copy issued has landed, and every MMA that read one is done
+        for (int j = i > S ? i - S : 0; j < i; ++j)
+          mbar_wait(empty + 8 * ((done + j) % S), ((done + j) / S) & 1u);
+      }
+    } else if (warp == 1) {
+      bool ok = true, here = false;
+      int i = 0;
+      for (; i < steps; ++i) {  // the whole warp, see mma_stage
+        const uint32_t it = done + i, s = it % S, ph = (it / S) & 1u;
+        if (!here) {
+          ok = mbar_wait(ready + 8 * s, ph, abort_addr, kWaitLimitNs);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+        }
+        tc_fence_after_sync();
+        const bool next =
+            mbar_test<1>(ready + 8 * ((it + 1) % S), ((it + 1) / S) & 1u);
+        const uint32_t sa = tmem_scales + s * P::kScaleCols;
+        mma_stage<FMT, 1>(
+            tmem, smem_desc_kmajor_sw128(base + s * P::kA),
+            smem_desc_kmajor_sw128(base + P::kOffB + s * P::kB),
+            idesc_f4<FMT>(kTile, NT, 0u),
+            idesc_f4<FMT>(kTile, NT, FMT == TQ_FMT_MX4 ? 2u : 0u), sa,
+            sa + P::kWords * 4, P::kBCols, i != 0 ? 1u : 0u, empty + 8 * s);
+        here = __all_sync(0xFFFFFFFFu, next);
+      }
+      if (ok) commit<1>(dfull);
+      for (int j = i > S ? i - S : 0; j < i; ++j)
+        mbar_wait(empty + 8 * ((done + j) % S), ((done + j) / S) & 1u);
+    } else if (warp < 6) {
+      move_scales(0);
     } else {
+      if (P::kGroups == 2 && warp < 10) move_scales(1);
       const int xw = warp - 6, xt = tid - 192;
       const int64_t k0 = (int64_t)st0 * kStageK;
       const int64_t k1 = k0 + (int64_t)steps * kStageK < a.k
@@ -460,7 +476,20 @@ __global__ void __launch_bounds__(kThreads, 2)
           uint32_t v[16];
           tmem_ld16(tmem + c + ((uint32_t)q << 21), v);
           tmem_ld_wait();
-          if constexpr (SRC == kPacked) {
+          if (SRC == kPacked && per == 8) {
+            const DigitArgs &D = a.digits;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int b = c / 8 + h;
+              if (8 * b >= rows) break;
+              const int64_t at = b0 / 8 + b;
+              float t = digit_sum<FMT>(&v[8 * h], D.exps[at]);
+              if (D.odd[at] && row0 + r < a.n)
+                t += odd_products<FMT>(D.x + at * D.ldx, (int)k0, (int)k1,
+                                       a.codes, a.wscales, wrow + r, a.k);
+              part[b * P::kPitch + r] = ok ? t : __int_as_float(0x7FC00000);
+            }
+          } else if constexpr (SRC == kPacked) {
 #pragma unroll
             for (int j = 0; j < 16; ++j)
               if (c + j < rows)
@@ -489,7 +518,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       __syncthreads();
     float g = a.wg != nullptr ? a.wg[expert] : 1.0f;
     if (SRC == kPacked && a.xg != nullptr) g *= *a.xg;
-    for (int i = tid + rank * kThreads; i < rows * kTile; i += ks * kThreads) {
+    for (int i = tid + rank * kThreads; i < rows / per * kTile;
+         i += ks * kThreads) {
       const int b = i / kTile, r = i % kTile;
       const uint32_t at = base + (uint32_t)(b * P::kPitch + r) * 4;
       float v = 0.0f;
@@ -511,7 +541,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       v *= g;
       if (row0 + r < a.n) {
-        const int64_t row = a.ids != nullptr ? s_rows[first + b] : b0 + b;
+        const int64_t row =
+            a.ids != nullptr ? s_rows[first + b] : b0 / per + b;
         if (a.y_bf16)
           static_cast<__nv_bfloat16 *>(a.y)[row * a.ldy + row0 + r] =
               __float2bfloat16_rn(v);
@@ -798,8 +829,9 @@ cudaError_t decode_f4_experts(const WeightsView &w, int n_experts,
 
 cudaError_t decode_f4_packed(const WeightsView &w, const WeightsView &x,
                              void *y, int64_t ldy, int y_type,
-                             cudaStream_t stream) {
+                             const DigitArgs &digits, cudaStream_t stream) {
   DecodeArgs a = weight_args(w);
+  a.digits = digits;
   a.xscales = reinterpret_cast<const uint8_t *>(x.scales);
   a.xg = x.lut;
   a.y = y;

@@ -42,14 +42,27 @@ __global__ void __launch_bounds__(256)
   const int64_t row = blockIdx.x;
   const __nv_bfloat16 *p = x + row * ldx;
   uint32_t m = 0, odd = 0;
-  for (int i = threadIdx.x * 8; i < k; i += 2048) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4 *>(p + i));
-    uint32_t t = max_mag8(w);
-    if (t >= 0x7F80u) {
-      odd = 1;
-      t = max_mag8(only_finite8(w));
+  // this block's values first, they are needed again
+  const int at = blockIdx.y * 2048 + threadIdx.x * 8;
+  uint4 w = make_uint4(0, 0, 0, 0);
+  if (at < k) w = __ldg(reinterpret_cast<const uint4 *>(p + at));
+  for (int i = threadIdx.x * 8; i < k; i += 4 * 2048) {
+    uint4 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = make_uint4(0, 0, 0, 0);
+      if (i + 2048 * j < k)
+        v[j] = __ldg(reinterpret_cast<const uint4 *>(p + i + 2048 * j));
     }
-    m = max(m, t);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t t = max_mag8(v[j]);
+      if (t >= 0x7F80u) {
+        odd = 1;
+        t = max_mag8(only_finite8(v[j]));
+      }
+      m = max(m, t);
+    }
   }
   __shared__ uint32_t s_m[8], s_odd[8];
   m = __reduce_max_sync(0xFFFFFFFFu, m);
@@ -70,9 +83,6 @@ __global__ void __launch_bounds__(256)
     odds[row] = (int)odd;
   }
   // k is a multiple of 32: the lanes of a block are in or out together
-  const int at = blockIdx.y * 2048 + threadIdx.x * 8;
-  uint4 w = make_uint4(0, 0, 0, 0);
-  if (at < k) w = __ldg(reinterpret_cast<const uint4 *>(p + at));
   if (odd) w = only_finite8(w);
   uint32_t b = max_mag8(w);
   b = max(b, __shfl_xor_sync(0xFFFFFFFFu, b, 1));
@@ -97,9 +107,20 @@ __global__ void __launch_bounds__(256)
 
 }  // namespace
 
-// 0 where the plain kernels do as well.
+// 0 where the plain kernels do as well. Measured (us; plain, digits):
+//   MX4  21504 x 5376 batch 4: 23, 16.5; 16: 43, 23; 64: 113, 40
+//        5376 x 21504 batch 4: 28, 20; 8192 x 5376 batch 4: 13.5, 11
+//        4096 x 4096 batch 8: 6.7, 11; 1024 x 2048 batch 64: 14.4, 12
+//   NV4  21504 x 5376 batch 4: 29, 20; 16: 42, 28; 64: 107, 56
+//        5376 x 21504 batch 4: 22.6, 24; 16: 31, 37; 64: 76, 66
+// The second launch costs 4 us, and long rows of x cost more digits for the
+// same weights, which the larger part of NV4 shows.
 int64_t digits_f4_workspace(const WeightsView &w, int64_t batch) {
-  if (batch < 16 || !decode_f4_supported(w, 1)) return 0;
+  const int64_t weights = w.n * w.k;
+  const bool large = batch >= 3 && weights >= (1 << 25) &&
+                     (w.format == TQ_FMT_MX4 || w.n >= w.k);
+  const bool wide = batch >= 32 && weights >= (1 << 21);
+  if (!(large || wide) || !decode_f4_supported(w, 1)) return 0;
   return layout_of(w.format, batch, w.k).total;
 }
 
@@ -123,8 +144,9 @@ cudaError_t digits_f4(const WeightsView &w, const __nv_bfloat16 *x,
     u.codes = workspace + L.codes;
     u.scales = reinterpret_cast<const uint16_t *>(workspace + L.scales);
     u.lut = nullptr;
-    if ((e = product_f4_digits(w, u, exps, odd, x + b * ldx, ldx, y + b * ldy,
-                               ldy, stream)) != cudaSuccess)
+    DigitArgs digits = {exps, odd, x + b * ldx, ldx};
+    if ((e = product_f4(w, u, y + b * ldy, ldy, TQ_Y_F32, digits, stream)) !=
+        cudaSuccess)
       return e;
   }
   return cudaSuccess;

@@ -132,7 +132,8 @@ __device__ __forceinline__ float digit_sum(const uint32_t *d, int X) {
   for (int i = 6; i >= 0; --i)
     t = FMT == TQ_FMT_MX4 ? t + __uint_as_float(d[i])
                           : fmaf(t, 0.125f, __uint_as_float(d[i]));
-  return scalbnf(t, X - (FMT == TQ_FMT_MX4 ? 127 : 136));
+  if (FMT == TQ_FMT_NV4) t *= 0.001953125f;  // 2^-9
+  return t * __uint_as_float((uint32_t)X << 23);
 }
 
 // One weight, for the rows of x that hold NaN or Inf.
@@ -164,6 +165,15 @@ __device__ __noinline__ float odd_products(const __nv_bfloat16 *x, int k0,
   }
   return t;
 }
+
+// Rows of a packed operand that are digits: every 8 of them belong to one row
+// of x. exps null: they are not.
+struct DigitArgs {
+  const int *exps;  // exponent of each row of x
+  const int *odd;   // whether it holds NaN or Inf
+  const __nv_bfloat16 *x;
+  int64_t ldx;
+};
 
 }  // namespace f4
 }  // namespace tq
