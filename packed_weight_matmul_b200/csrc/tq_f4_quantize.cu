@@ -5,18 +5,25 @@
 // Formats (MX) Specification" v1.0, section 6.3, for MX4):
 //   MX4  scale 2^E, E = floor(log2 max|v|) - 2; code = E2M1_RNE(v 2^-E)
 //   NV4  scale s g, s = E4M3_RNE(max|v| / (6 g)); code = E2M1_RNE(v / (s g))
-// A lane holds 8 values (one 16-byte load), so a block of 32 (16) is 4 (2)
-// neighbouring lanes and its maximum two (one) shuffles; codes leave as one
-// 4-byte store per lane. Bound by HBM: 2 + 0.53 bytes per value.
+// MX4: a lane holds 8 values (one 16-byte load), a block of 32 is 4 neighbouring
+// lanes and its maximum two shuffles. NV4: a lane holds a whole block of 16 (two
+// loads), since what a block costs (below) would be paid twice otherwise. Bound
+// by HBM, 2 + 0.53 bytes per value, and nearly as much by arithmetic.
 //
 // Every decision equals exact arithmetic. MX4: v 2^-E is exact in fp32. NV4:
-// quotients are taken as products with a reciprocal (relative error below
-// 2^-21), and one within 2^-19 of a border t between two results is settled
-// by the sign of v - t d, d = s g (or 6 g): d as the unrounded sum of two fp32
-// numbers makes it exact in two fused multiply-adds. Such quotients are not
-// rare: with g = max|W| / 2688 and values of 8 significant bits, many lie at a
-// border but for the rounding of g (deciding them in fp64, a division each,
-// made the kernel 6 times slower than the MX4 one).
+// quotients are taken as products with a reciprocal, relative error below
+// 2^-21, so only those next to a border t between two codes need more. Such
+// quotients are not rare: with g = max|W| / 2688 and values of 8 significant
+// bits, many lie at a border but for the rounding of g. But at a border v is
+// close to t d, d = s g, t one of 1, 3, 5, 7 (times a power of two) and v of 8
+// bits, and two different v / t differ by 2^-13 or more: all the close ones of
+// a block have one v / t, on one side of d. So a block asks once, per t,
+// whether t d is close to an 8-bit number, takes the side from the sign of
+// v - t d (exact in two fused multiply-adds, d held as an unrounded sum), and
+// moves its reciprocal by 2^-19 to that side; on a tie it clears the last bits
+// of the quotients instead. (8192 x 5376: 26 us; with each close
+// quotient decided by itself 36 us, in fp64 133 us.) The block scale
+// is settled in the same manner, quotient by quotient.
 #include "tq_f4.cuh"
 
 namespace tq {
@@ -153,22 +160,33 @@ __device__ __forceinline__ uint32_t nv4_scale(float top, const Nv4 &s) {
   return b;
 }
 
+// Words of 8 values that a lane takes at once.
 template <int FMT>
-__device__ __forceinline__ void quantize8(const uint4 &w, const Nv4 &s,
-                                          uint32_t *codes, uint32_t *byte,
-                                          bool *bad) {
-  uint32_t m = max_mag8(w);
-  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-  if (FMT == TQ_FMT_MX4) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+constexpr int kWords = FMT == TQ_FMT_MX4 ? 1 : 2;
+
+template <int FMT>
+__device__ __forceinline__ void quantize_words(const uint4 (&w)[kWords<FMT>],
+                                               const Nv4 &s,
+                                               uint32_t (&codes)[kWords<FMT>],
+                                               uint32_t *byte, bool *bad) {
+  uint32_t m = max_mag8(w[0]);
+  if constexpr (FMT == TQ_FMT_MX4) {
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+  } else {
+    m = max(m, max_mag8(w[1]));
+  }
   if (m >= 0x7F80u) {  // NaN or Inf in the block
     *bad = true;
-    *codes = 0;
+#pragma unroll
+    for (int h = 0; h < kWords<FMT>; ++h) codes[h] = 0;
     *byte = FMT == TQ_FMT_MX4 ? 0xFFu : 0x7Fu;
     return;
   }
-  float inv, q[8];
+  float inv;
   const float top = __uint_as_float(m << 16);
   float sf = 0.0f;
+  bool tie = false;
   if (FMT == TQ_FMT_MX4) {
     // bf16 exponent field f: floor(log2 top) = f - 127, so the byte is
     // f - 2; subnormal maxima (f = 0) clamp to 0 as well
@@ -179,46 +197,59 @@ __device__ __forceinline__ void quantize8(const uint4 &w, const Nv4 &s,
     *byte = nv4_scale(top, s);
     sf = e4m3_to_f32(*byte);
     inv = sf == 0.0f ? 0.0f : __fdividef(s.inv_g, sf);
-  }
-  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    asm("{\n .reg .b64 a, b;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %4};\n"
-        " mul.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, a;\n}"
-        : "=f"(q[2 * i]), "=f"(q[2 * i + 1])
-        : "f"(bf16_lo(v[i])), "f"(bf16_hi(v[i])), "f"(inv));
-  }
-  if (FMT == TQ_FMT_NV4) {
-    // Borders of E2M1 have at most 3 significant bits: their low 21 bits are
-    // clear.
     const Two d = two_product(sf, s.g);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (__builtin_expect(near_border<21>(q[i]), 0))
-        q[i] = settle<21>(q[i], i & 1 ? bf16_hi(v[i / 2]) : bf16_lo(v[i / 2]),
-                          d);
+    for (int t = 1; t < 8; t += 2) {
+      const uint32_t u = __float_as_uint((float)t * d.hi) + 64u;
+      if ((u & 0xFFFFu) < 128u) {  // within 64 units of an 8-bit number
+        const float r = fmaf(-(float)t, d.lo,
+                             fmaf(-(float)t, d.hi,
+                                  __uint_as_float(u & 0xFFFF0000u)));
+        if (r == 0.0f)
+          tie = true;
+        else
+          inv = __uint_as_float(__float_as_uint(inv) + (r > 0.0f ? 16u : -16u));
+        break;
+      }
     }
   }
-  *codes = e2m1x8(q);
-  if (FMT == TQ_FMT_NV4 && s.exact && sf != 0.0f) {
-    const double d = (double)sf * (double)s.g;
-    uint32_t c = 0;
-#pragma unroll 1
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t h = i < 2 ? v[0] : i < 4 ? v[1] : i < 6 ? v[2] : v[3];
-      c |= e2m1_of_f64(i & 1 ? bf16_hi(h) : bf16_lo(h), d) << (4 * i);
+#pragma unroll
+  for (int h = 0; h < kWords<FMT>; ++h) {
+    const uint32_t v[4] = {w[h].x, w[h].y, w[h].z, w[h].w};
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      asm("{\n .reg .b64 a, b;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %4};\n"
+          " mul.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, a;\n}"
+          : "=f"(q[2 * i]), "=f"(q[2 * i + 1])
+          : "f"(bf16_lo(v[i])), "f"(bf16_hi(v[i])), "f"(inv));
     }
-    *codes = c;
+    if (FMT == TQ_FMT_NV4 && tie) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        q[i] = __uint_as_float((__float_as_uint(q[i]) + 8u) & ~15u);
+    }
+    codes[h] = e2m1x8(q);
+    if (FMT == TQ_FMT_NV4 && s.exact && sf != 0.0f) {
+      const double d = (double)sf * (double)s.g;
+      uint32_t c = 0;
+#pragma unroll 1
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t x = i < 2 ? v[0] : i < 4 ? v[1] : i < 6 ? v[2] : v[3];
+        c |= e2m1_of_f64(i & 1 ? bf16_hi(x) : bf16_lo(x), d) << (4 * i);
+      }
+      codes[h] = c;
+    }
   }
 }
 
 // `rows` rows of `units` 16-byte units (8 values), `pitch` units apart; a dense
 // matrix comes as one row. A block takes kPer * 256 consecutive units of a
-// row, a thread every 256th of them, so that kPer loads are in flight.
+// row; a thread's kPer loads are in flight together.
 constexpr int kPer = 4, kChunk = 256 * kPer;
 
 template <int FMT>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 5)
     quantize_f4_kernel(const uint4 *__restrict__ W, int64_t rows,
                        int64_t units, int64_t pitch,
                        uint32_t *__restrict__ codes,
@@ -235,28 +266,39 @@ __global__ void __launch_bounds__(256)
   }
   for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
     const uint4 *src = W + row * pitch;
-    for (int64_t u0 = (int64_t)blockIdx.x * kChunk + threadIdx.x;
-         u0 - threadIdx.x < units; u0 += (int64_t)gridDim.x * kChunk) {
-      uint4 w[kPer];
+    // whole warps run the shuffles: the loop goes by the block's first unit
+    for (int64_t first = (int64_t)blockIdx.x * kChunk; first < units;
+         first += (int64_t)gridDim.x * kChunk) {
+      const int64_t u0 = first + threadIdx.x * kWords<FMT>;
+      constexpr int N = kWords<FMT>, kRounds = kPer / N;
+      uint4 w[kRounds][N];
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        w[i] = make_uint4(0, 0, 0, 0);
-        if (u0 + 256 * i < units) w[i] = __ldg(src + u0 + 256 * i);
+      for (int i = 0; i < kRounds; ++i) {
+        const int64_t u = u0 + 256 * N * i;
+#pragma unroll
+        for (int h = 0; h < N; ++h) {
+          w[i][h] = make_uint4(0, 0, 0, 0);
+          if (u < units) w[i][h] = __ldg(src + u + h);  // units: a multiple of N
+        }
       }
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int64_t u = u0 + 256 * i;
-        uint32_t c, b;
-        quantize8<FMT>(w[i], s, &c, &b, &bad);
+      for (int i = 0; i < kRounds; ++i) {
+        const int64_t u = u0 + 256 * N * i;
+        uint32_t c[N], b;
+        quantize_words<FMT>(w[i], s, c, &b, &bad);
         if (u >= units) continue;
-        if (bad_g) {
-          c = 0;
-          b = 0x7Fu;
-        }
-        constexpr int kLanes = f4_block(FMT) / 8;
         const int64_t at = row * units + u;
-        codes[at] = c;
-        if (threadIdx.x % kLanes == 0) scales[at / kLanes] = (uint8_t)b;
+        if constexpr (FMT == TQ_FMT_MX4) {
+          codes[at] = c[0];
+          if (threadIdx.x % 4 == 0) scales[at / 4] = (uint8_t)b;
+        } else {
+          if (bad_g) {
+            c[0] = c[N - 1] = 0;
+            b = 0x7Fu;
+          }
+          *reinterpret_cast<uint2 *>(codes + at) = make_uint2(c[0], c[N - 1]);
+          scales[at / 2] = (uint8_t)b;
+        }
       }
     }
   }

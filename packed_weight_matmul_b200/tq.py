@@ -435,7 +435,7 @@ def _f4_tensor(t, dtypes, what):
         raise TqError(TQ_ERR_INVALID_ARG, f"{what}: not on the current device")
     if t.dtype not in dtypes:
         raise TqError(TQ_ERR_INVALID_ARG, f"{what}: {t.dtype}")
-    if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise TqError(TQ_ERR_INVALID_ARG, f"{what}: rows are not dense")
 
 
@@ -444,6 +444,7 @@ def _rows(t):
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
+_BF16, _F32 = (torch.bfloat16,), (torch.float32,)
 _U8 = (torch.uint8, torch.int8, torch.float8_e8m0fnu, torch.float8_e4m3fn)
 
 
@@ -455,15 +456,15 @@ def tq_quantize_f4(W, fmt, codes_out, scales_out, tensor_scale=None,
     [n][k/16] (TQ_FMT_NV4). NV4: tensor_scale is read when scale_given, else
     written."""
     n, k = W.shape
-    _f4_tensor(W, (torch.bfloat16,), "tq_quantize_f4: W")
-    _f4_tensor(codes_out, (torch.uint8,), "tq_quantize_f4: codes_out")
+    _f4_tensor(W, _BF16, "tq_quantize_f4: W")
+    _f4_tensor(codes_out, _U8, "tq_quantize_f4: codes_out")
     _f4_tensor(scales_out, _U8, "tq_quantize_f4: scales_out")
-    if codes_out.numel() < n * (k // 2) or not codes_out.is_contiguous() or \
-            scales_out.numel() < n * (k // F4_BLOCK.get(fmt, 16)) or \
+    if codes_out.numel() * 2 < n * k or not codes_out.is_contiguous() or \
+            scales_out.numel() * F4_BLOCK.get(fmt, 16) < n * k or \
             not scales_out.is_contiguous():
         raise TqError(TQ_ERR_SHAPE, "tq_quantize_f4: outputs")
     if tensor_scale is not None:
-        _f4_tensor(tensor_scale, (torch.float32,), "tq_quantize_f4: scale")
+        _f4_tensor(tensor_scale, _F32, "tq_quantize_f4: scale")
     st = _lib.tq_quantize_f4(W.data_ptr(), n, k, _rows(W), fmt,
                              codes_out.data_ptr(), scales_out.data_ptr(),
                              _ptr(tensor_scale), int(bool(scale_given)),
