@@ -99,6 +99,29 @@ int64_t digits_f4_workspace(const WeightsView &w, int64_t batch);
 cudaError_t digits_f4(const WeightsView &w, const __nv_bfloat16 *x,
                       int64_t batch, int64_t ldx, float *y, int64_t ldy,
                       uint8_t *workspace, cudaStream_t stream);
+// Clusters of `ks` CTAs that are resident together; 0: not known.
+inline int max_clusters(const void *kern, int ks, int threads, size_t smem) {
+  // An error already pending belongs to the caller: leave it.
+  if (cudaPeekAtLastError() != cudaSuccess) return 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ks);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)ks;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+    cudaGetLastError();  // the query's own error
+    return 0;
+  }
+  return n;
+}
+
 // The product with packed rows of x, which may be digits (tq_f4_gemm.cu).
 cudaError_t product_f4(const WeightsView &w, const WeightsView &x, void *y,
                        int64_t ldy, int y_type, const f4::DigitArgs &digits,

@@ -79,7 +79,6 @@ struct DecodePlan {
   static constexpr uint32_t kSmem = kOffBar + 256 + 1024;
   static constexpr int kPitch = kTile + 4;  // of the partial tile
   static_assert(kRows * kPitch * 4 <= kOffS, "partial tile");
-  static constexpr int kStaged = SRC == kBf16 && kRows > 8 ? 2 : 1;  // per warp
   static_assert(SRC == kPacked || kRows <= 16, "rows per warp");
 };
 
@@ -348,13 +347,14 @@ __global__ void __launch_bounds__(kThreads, 2)
         return a.x + (a.ids != nullptr ? s_rows[first + r] : b0 + r) * a.ldx;
       };
       if constexpr (SRC == kBf16) {
+        constexpr int kStaged = P::kRows > 8 ? 2 : 1;  // rows of a warp
         // the first values to convert, on their way during what follows
         const int mine = xw % per_stage;
-        uint4 next[P::kStaged];
+        uint4 next[kStaged];
         auto load = [&](int i) {
           const int64_t k = k0 + (int64_t)i * kStageK + 8 * lane;
 #pragma unroll
-          for (int j = 0; j < P::kStaged; ++j) {
+          for (int j = 0; j < kStaged; ++j) {
             const int r = mine + 8 * j;
             next[j] = make_uint4(0, 0, 0, 0);
             if (r < rows && i < steps && k < k1)
@@ -422,19 +422,19 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll 1
         for (; i < steps; i += at_once) {
           const uint32_t it = done + i, s = it % S, ph = (it / S) & 1u;
-          uint4 now[P::kStaged];
+          uint4 now[kStaged];
 #pragma unroll
-          for (int j = 0; j < P::kStaged; ++j) now[j] = next[j];
+          for (int j = 0; j < kStaged; ++j) now[j] = next[j];
           load(i + at_once);
           bool ok = mbar_wait(empty + 8 * s, ph ^ 1u, abort_addr, kWaitLimitNs);
           ok = __all_sync(0xFFFFFFFFu, ok);
           if (!ok) break;
 #pragma unroll 1
-          for (int j = 0; j < P::kStaged; ++j) {
+          for (int j = 0; j < kStaged; ++j) {
             const int r = mine + 8 * j;
             if (r >= rows) break;
             uint4 w = now[0];
-            if (P::kStaged > 1 && j == 1) w = now[P::kStaged - 1];
+            if (kStaged > 1 && j == 1) w = now[kStaged - 1];
             if (s_odd[r]) w = only_finite8(w);
             uint32_t m = max_mag8(w);
             m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
@@ -685,27 +685,9 @@ int resident(int ks, int dev) {
     const int v = known[dev][ks].load(std::memory_order_relaxed);
     if (v != 0) return v;
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ks);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = P::kSmem;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ks;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  int n = 0;
-  if (cudaOccupancyMaxActiveClusters(
-          &n,
-          reinterpret_cast<const void *>(decode_f4_kernel<FMT, NT, SRC>),
-          &cfg) != cudaSuccess ||
-      n < 1) {
-    cudaGetLastError();
-    n = 1;
-  }
-  if (dev < 16) known[dev][ks].store(n, std::memory_order_relaxed);
+  const int n = max_clusters(reinterpret_cast<const void *>(decode_f4_kernel<FMT, NT, SRC>),
+                             ks, kThreads, P::kSmem);
+  if (dev < 16 && n > 0) known[dev][ks].store(n, std::memory_order_relaxed);
   return n;
 }
 
