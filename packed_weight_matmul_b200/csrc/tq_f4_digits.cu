@@ -39,11 +39,11 @@ __global__ void __launch_bounds__(256)
                   int *__restrict__ exps, int *__restrict__ odds) {
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t row = blockIdx.x;
+  const int64_t row = blockIdx.y;
   const __nv_bfloat16 *p = x + row * ldx;
   uint32_t m = 0, odd = 0;
   // this block's values first, they are needed again
-  const int at = blockIdx.y * 2048 + threadIdx.x * 8;
+  const int at = blockIdx.x * 2048 + threadIdx.x * 8;
   uint4 w = make_uint4(0, 0, 0, 0);
   if (at < k) w = __ldg(reinterpret_cast<const uint4 *>(p + at));
   for (int i = threadIdx.x * 8; i < k; i += 4 * 2048) {
@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(256)
     odd |= s_odd[i];
   }
   const int X = max((int)(m >> 7), 1);
-  if (blockIdx.y == 0 && threadIdx.x == 0) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
     exps[row] = X;
     odds[row] = (int)odd;
   }
@@ -130,7 +130,8 @@ cudaError_t digits_f4(const WeightsView &w, const __nv_bfloat16 *x,
   const Layout L = layout_of(w.format, batch, w.k);
   for (int64_t b = 0; b < batch; b += L.rows) {
     const int64_t rows = batch - b < L.rows ? batch - b : L.rows;
-    const dim3 grid((unsigned)rows, (unsigned)((w.k + 2047) / 2048));
+    // (the second dimension ends at 65535)
+    const dim3 grid((unsigned)((w.k + 2047) / 2048), (unsigned)rows);
     int *exps = reinterpret_cast<int *>(workspace + L.exps);
     int *odd = reinterpret_cast<int *>(workspace + L.odd);
     auto kern = w.format == TQ_FMT_MX4 ? digits_kernel<TQ_FMT_MX4>

@@ -435,7 +435,7 @@ def _f4_tensor(t, dtypes, what):
         raise TqError(TQ_ERR_INVALID_ARG, f"{what}: not on the current device")
     if t.dtype not in dtypes:
         raise TqError(TQ_ERR_INVALID_ARG, f"{what}: {t.dtype}")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+    if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
         raise TqError(TQ_ERR_INVALID_ARG, f"{what}: rows are not dense")
 
 

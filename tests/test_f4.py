@@ -145,6 +145,41 @@ def test_linear_refusals(tq):
     assert call(w=desc(tq, n_rows=0), ldy=0) == tq.TQ_OK
 
 
+def test_linear_workspace_refusals(tq):
+    big = desc(tq, n_rows=8192, k_cols=8192)
+
+    def need(w, b):
+        return tq.lib().tq_linear_workspace(C.byref(w), b)
+    # digit rows of x: 8 rows of codes and scales each, and two words per row
+    for b in (3, 64, 512):
+        assert need(big, b) >= b * (8 * 8192 * 9 // 16 + 8)
+    assert need(big, 5000) == need(big, 512)  # 512 rows at a time
+    assert need(big, 1) == 0 and need(big, 0) == 0 and need(big, -1) == 0
+    assert need(desc(tq), 64) == 0
+    assert need(desc(tq, n_rows=8192, k_cols=8192, codes=None), 64) == 0
+    assert need(desc(tq, n_rows=0, k_cols=8192), 64) == 0
+    a = tq.tq_weights(format=tq.TQ_FMT_A, group=64, planes=1, rows_per_scale=0,
+                      n_rows=8192, k_cols=8192, codes=0x10000, scales=0x20000)
+    assert need(a, 64) == 0
+    assert tq.lib().tq_linear_workspace(None, 64) == 0
+
+    def call(x=0x40000, b=64, ldx=8192, y=0x50000, ldy=8192, ws=0x60000,
+             size=0, w=big):
+        return tq.lib().tq_linear_ws(C.byref(w), x, b, ldx, y, ldy, ws, size,
+                                     None)
+    size = need(big, 64)
+    assert call(ws=0x60080, size=size) == tq.TQ_ERR_ALIGNMENT
+    assert call(x=None) == tq.TQ_ERR_INVALID_ARG
+    assert call(y=None) == tq.TQ_ERR_INVALID_ARG
+    assert call(b=0) == tq.TQ_ERR_INVALID_ARG
+    assert call(ldx=8184) == tq.TQ_ERR_SHAPE
+    assert call(ldy=8191) == tq.TQ_ERR_SHAPE
+    assert call(x=0x40008) == tq.TQ_ERR_ALIGNMENT
+    assert call(ldx=8196) == tq.TQ_ERR_ALIGNMENT
+    assert call(y=0x50002) == tq.TQ_ERR_ALIGNMENT
+    assert call(w=desc(tq, n_rows=0), b=1, ldx=128) == tq.TQ_OK
+
+
 def test_product_refusals(tq):
     w, x = desc(tq), desc(tq, n_rows=3)
 

@@ -387,6 +387,159 @@ def test_product_nan_scales(fmt, b):
     assert torch.equal(y[keep].double(), ref[keep])
 
 
+# ---- bf16 rows written as digit rows ------------------------------------------------
+
+def linear_ws(w, x, used=True):
+    """tq_linear_ws with a workspace that was filled with 0xFF before."""
+    tq, b = U.tq(), x.shape[0]
+    need = tq.lib().tq_linear_workspace(w.desc, b)
+    assert (need > 0) == used
+    ws = torch.full((need + 512,), 0xFF, dtype=torch.uint8, device=U.DEV)
+    y = torch.full((b, w.n), float("nan"), device=U.DEV)
+    st = tq.lib().tq_linear_ws(
+        w.desc, x.data_ptr(), b, x.stride(0), y.data_ptr(), w.n,
+        ws.data_ptr(), need, torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert st == tq.TQ_OK and (ws[need:] == 0xFF).all()
+    return y
+
+
+# n, k, batches: many weights from 3 rows on (NV4: n >= k), fewer weights from
+# 32 rows on; ragged tiles, a last stage of 32 to 160 codes, several chunks of
+# 512 rows
+DIGITS = [(MX4, 4096, 8192, (3, 5, 8, 9, 20)), (MX4, 1003, 33472, (4, 7)),
+          (NV4, 8200, 4128, (3, 8, 13, 33)), (NV4, 5800, 5792, (5, 17)),
+          (MX4, 1040, 2080, (32, 33, 65, 130)), (NV4, 1040, 2080, (32, 64, 97)),
+          (MX4, 1100, 1952, (600, 1030)), (NV4, 1100, 1952, (513,))]
+
+
+@pytest.mark.parametrize("fmt,n,k,batches", DIGITS)
+def test_digit_rows_exact(fmt, n, k, batches):
+    """Integers times exact packages, with rows of zeros, NaN and Inf."""
+    codes, scales = exact_package(fmt, n, k, n + k)
+    if k > 20000:  # partial sums below 2^22 in steps of 1/4
+        codes &= 11
+    codes[:, 100] = 2  # no 0 * Inf in the checked column
+    codes[3] = 0
+    codes[3, 100] = 1
+    scales[n - 2, 1] = 255 if fmt == MX4 else 127
+    w64 = F.values(codes, scales, fmt)
+    w = weights(fmt, F.pack(codes), scales, None)
+    for b in batches:
+        x = integers(b, k, b)
+        x[b // 2] = 0
+        x[1, 100] = float("inf")
+        if b > 3:
+            x[2, 31] = float("nan")
+            x[3, 100] = -float("inf")
+        ref = x.double() @ w64.t()
+        y = linear_ws(w, x)
+        nan = torch.isnan(ref)
+        assert torch.equal(nan, torch.isnan(y)), f"batch {b}"
+        assert torch.equal(y[~nan].double(), ref[~nan]), f"batch {b}"
+        again = run_linear(w, x)  # the binding brings its own workspace
+        assert torch.equal(again[~nan], y[~nan])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("n,k,b", [(8192, 4096, 6), (1040, 2080, 40),
+                                   (1100, 1952, 515)])
+def test_digit_rows_range(fmt, n, k, b):
+    """x over many powers of two inside a row, rows at both ends of the
+    range, from rows with a padded stride."""
+    W = sample(n, k, 31)
+    codes, scales, g, _ = quantize(W, fmt)
+    wide = torch.full((b, k + 40), float("nan"), dtype=torch.bfloat16,
+                      device=U.DEV)
+    x = wide[:, :k]
+    x.copy_(torch.randn(b, k, generator=gen(3), device=U.DEV) * torch.exp2(
+        torch.randint(-30, 5, (b, k), generator=gen(4), device=U.DEV).float()))
+    x[0] = (x[0].double() * 2.0 ** 100).bfloat16()
+    x[1] = (x[1].double() * 2.0 ** -110).bfloat16()
+    w = weights(fmt, codes, scales, g)
+    w64 = F.values(F.unpack_codes(codes), scales, fmt)
+    if g is not None:
+        w64 = w64 * g.double()
+    y = linear_ws(w, x)
+    F.check(y, x.double() @ w64.t(), F.sum_bound(w64, x.double(), k))
+    assert torch.equal(y, linear_ws(w, x))  # the same bits every time
+
+
+def test_digit_rows_small_workspace():
+    """One byte too few: the plain kernels, the workspace untouched."""
+    tq = U.tq()
+    codes, scales = exact_package(MX4, 1040, 2080, 1)
+    w = weights(MX4, F.pack(codes), scales)
+    x = integers(40, 2080, 2)
+    need = tq.lib().tq_linear_workspace(w.desc, 40)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device=U.DEV)
+    y = torch.full((40, 1040), float("nan"), device=U.DEV)
+    for ptr, size in ((ws.data_ptr(), need - 1), (None, 0), (None, need)):
+        y.fill_(float("nan"))
+        assert tq.lib().tq_linear_ws(w.desc, x.data_ptr(), 40, 2080,
+                                     y.data_ptr(), 1040, ptr, size,
+                                     None) == tq.TQ_OK
+        torch.cuda.synchronize()
+        assert torch.equal(y.double(),
+                           x.double() @ F.values(codes, scales, MX4).t())
+    assert (ws == 0xFF).all()
+
+
+def test_digit_rows_streams_and_graphs():
+    """Two streams at once, and two captured graphs replayed in turn, each
+    with scratch of its own."""
+    tq = U.tq()
+    codes, scales = exact_package(NV4, 1040, 2080, 5)
+    w64 = F.values(codes, scales, NV4)
+    w = weights(NV4, F.pack(codes), scales)
+    xs = [integers(b, 2080, b) for b in (40, 70)]
+    ys = [torch.zeros(x.shape[0], 1040, device=U.DEV) for x in xs]
+    refs = [x.double() @ w64.t() for x in xs]
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i in (0, 1):
+            tq.tq_linear(w, xs[i], ys[i], stream=sides[i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(y.double(), r) for y, r in zip(ys, refs))
+    graphs = []
+    for i in (0, 1):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            tq.tq_linear(w, xs[i], ys[i])
+        graphs.append(g)
+    for i in (0, 1, 1, 0):
+        ys[i].zero_()
+        xs[i].copy_(-xs[i])
+        refs[i] = -refs[i]
+        graphs[i].replay()
+        tq.tq_linear(w, xs[1 - i], ys[1 - i])
+        torch.cuda.synchronize()
+        assert all(torch.equal(y.double(), r) for y, r in zip(ys, refs))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("n", [40, 200, 600])
+def test_product_with_itself(fmt, n):
+    """x and w may be the same matrix."""
+    c, s = exact_package(fmt, n, 544, 3)
+    w = weights(fmt, F.pack(c), s, None)
+    w64 = F.values(c, s, fmt)
+    assert torch.equal(run_product(w, w, torch.float32).double(),
+                       w64 @ w64.t())
+
+
+def test_scalar_tensor_scale():
+    """The tensor scale may be a tensor without dimensions."""
+    tq, W = U.tq(), sample(4, 64, 1)
+    c = torch.empty(4, 32, dtype=torch.uint8, device=U.DEV)
+    s = torch.empty(4, 4, dtype=torch.uint8, device=U.DEV)
+    g = torch.empty((), device=U.DEV)
+    tq.tq_quantize_f4(W, NV4, c, s, g)
+    torch.cuda.synchronize()
+    assert g.item() == F.tensor_scale(W).item()
+
+
 # ---- experts ------------------------------------------------------------------------
 
 def run_experts(fmt, E, n, k, ids, seed, pad=0):
@@ -429,6 +582,22 @@ def test_experts(fmt, E, n, k, t):
     assert run_experts(fmt, E, n, k, ids, 7) == 0
     assert run_experts(fmt, E, n, k, ids, 8, pad=8) == 0
     assert run_experts(fmt, E, n, k, [E - 1] * t, 9) == 0  # all to one
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("E,n,k,t", [(3, 40, 96, 2500), (40, 20, 64, 4100),
+                                     (2000, 3, 32, 1500), (5000, 2, 32, 5200),
+                                     (5000, 2, 32, 3000), (128, 70, 288, 500)])
+def test_experts_many_rows(fmt, E, n, k, t):
+    """More ids than are looked through at once; more experts than the map of
+    the slots holds; an expert that takes nearly all rows."""
+    rng = np.random.default_rng(E + t)
+    ids = rng.integers(0, E, t)
+    assert run_experts(fmt, E, n, k, ids.tolist(), 7) == 0
+    ids[rng.random(t) < 0.9] = E // 2
+    ids[[5, t - 1]] = E, -1
+    assert run_experts(fmt, E, n, k, ids.tolist(), 8) == \
+        U.tq().TQ_ERR_INVALID_ARG
 
 
 @pytest.mark.parametrize("fmt", FMTS)
