@@ -163,8 +163,10 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
 
   pdl_launch_dependents();
   // Hint the L2 cache with this warp's codes, so that they are on their way
-  // while the kernel before finishes: lane r takes row r of the slice.
-  if (lane <= last && count > 0) {
+  // while the kernel before finishes: lane r takes row r of the slice. Not for
+  // experts, most of whose CTAs start long after that kernel's end: 500 rows
+  // over 128 experts of 768 x 2048 (NV4) 46 us with it, 42 us without.
+  if (a.ids == nullptr && lane <= last && count > 0) {
     const int64_t from = (int64_t)st0 * (kStageK / 2);
     const int64_t to = (int64_t)st1 * (kStageK / 2);
     const int64_t bytes = (to < code_pitch ? to : code_pitch) - from;
@@ -216,9 +218,15 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 
+  auto start = [&] {
+#pragma unroll 1
+    for (int p = 0; p < kRing - 1; ++p) issue(p, p);
+  };
+
   const float gw = a.g != nullptr ? a.g[expert] : 1.0f;
-  // `rows` <= NT rows of x, s_rows[base + i] each (or b0 + i): one pass
-  auto pass = [&](int base, int64_t b0, int rows) {
+  // `rows` <= NT rows of x, s_rows[base + i] each (or b0 + i): one pass;
+  // `started`: its first stages are on their way
+  auto pass = [&](int base, int64_t b0, int rows, bool started) {
     float acc[kTiles][4];
 #pragma unroll
     for (int i = 0; i < kTiles; ++i)
@@ -230,9 +238,7 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
 #pragma unroll
     for (int j = 0; j < P::kPer; ++j) ex[j] = -112;
 
-#pragma unroll 1
-    for (int p = 0; p < kRing - 1; ++p) issue(p, p);
-
+    if (!started) start();
     // Rows of x, kXK values of each per buffer. Thread tid holds units
     // tid + kThreads j, a warp's 32 units of one j lie in one row.
     const int64_t k_end =
@@ -240,7 +246,7 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
     const int buffers = (count + P::kXStages - 1) / P::kXStages;
     constexpr int kHeld = P::kPer < 4 ? P::kPer : 4;  // units in registers
     uint4 xr[kHeld];
-    auto load_x = [&](int i, int j0) {
+    auto load_x = [&](int i, int j0, uint4 (&xr)[kHeld]) {
       if (i >= buffers) return;
       const int64_t k0 = (int64_t)st0 * kStageK + (int64_t)i * P::kXK;
 #pragma unroll
@@ -311,7 +317,11 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
       return rose;
     };
 
-    if (P::kXBufs == 2) load_x(0, 0);
+    uint4 then[kHeld];  // the second buffer's, on their way with the first's
+    if (P::kXBufs == 2) {
+      load_x(0, 0, xr);
+      load_x(1, 0, then);
+    }
     for (int i = tid; i < P::kXBufs * (NT - rows) * (P::kXPitch / 16);
          i += kThreads) {
       const int b = i / ((NT - rows) * (P::kXPitch / 16));
@@ -324,7 +334,8 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
       publish(0);
       if (kShared) __syncthreads();
       any = convert(0, 0);
-      load_x(1, 0);
+#pragma unroll
+      for (int j = 0; j < kHeld; ++j) xr[j] = then[j];
       publish(1);
       any = __syncthreads_or(any);
     }
@@ -334,14 +345,14 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
       int rose = 0;
       if constexpr (P::kXBufs == 2) {
         rose = convert(i + 1, 0);
-        load_x(i + 2, 0);
+        load_x(i + 2, 0, xr);
       } else {
         // one buffer: filled between two barriers, while the other CTA of the
         // SM computes
         if (i > 0) __syncthreads();
 #pragma unroll
         for (int j = 0; j < P::kPer; j += kHeld) {
-          load_x(i, j);
+          load_x(i, j, xr);
           rose |= convert(i, j);
         }
         any = __syncthreads_or(rose);
@@ -577,7 +588,7 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
 
   if (a.ids == nullptr) {
     const int64_t b0 = (int64_t)blockIdx.y * NT;
-    pass(0, b0, (int)(a.batch - b0 < NT ? a.batch - b0 : NT));
+    pass(0, b0, (int)(a.batch - b0 < NT ? a.batch - b0 : NT), false);
     return;
   }
   // Rows of x that picked this expert, in ascending order (every CTA of the
@@ -586,6 +597,8 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
   // 768 x 2048, 2048 and 4096 rows: 83 and 145 us, against 137 and 430 us
   // with passes after every segment.
   int held = 0;
+  start();  // most experts have rows: the codes come while the ids are read
+  bool started = true;
   for (int64_t seg = 0; seg < a.batch; seg += kSegment) {
     constexpr int kPer = kSegment / kThreads;
     uint32_t hit = 0;  // bit j: id j of this thread
@@ -643,12 +656,15 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
     __syncthreads();
     held += s_count[kSegment / 32];
     if (held > kList - kSegment || seg + kSegment >= a.batch) {
-      for (int base = 0; base < held; base += NT)
-        pass(base, 0, held - base < NT ? held - base : NT);
+      for (int base = 0; base < held; base += NT) {
+        pass(base, 0, held - base < NT ? held - base : NT, started);
+        started = false;
+      }
       held = 0;
     }
     __syncthreads();  // the list and the counts have been read
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // Clusters of ks CTAs that are resident together, asked once per kernel, ks
