@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           });
         else
           each([&](uint32_t (&d)[kPieceWords], const uint8_t *p) {
-            load_piece_bytes(d, p, row_bytes - off);
+            load_piece_shifted(d, p, row_bytes - off);
           });
       };
       const int units = (steps + P::kUnitStages - 1) / P::kUnitStages;

@@ -13,21 +13,34 @@
 //
 // A tile is CG * 128 weight rows (M) times NT batch rows (N); CG = 2 pairs
 // the CTAs of a cluster on one tile (each holds its 128 weight rows and half
-// of the batch rows). Persistent, 18 warps per CTA:
+// of the batch rows). Persistent, 16 (pair, NV4) or 18 warps per CTA:
 //   warp 0       TMA producer: per stage of 256 k the 128-byte swizzled boxes
 //                of the weight rows and of this CTA's batch rows; it also
 //                allocates the tensor memory
 //   warp 1       MMA issuer (first CTA of a pair): 4 MMAs of K = 64 per stage;
 //                in the second CTA it passes "stage ready" on to the first
-//   warps 2-9    scales, two groups of four warps that take turns. A group
-//                reads the scales of every row for 4 stages (32 bytes of MX4,
-//                64 of NV4) into registers one turn ahead, lays them down
-//                row by row in shared memory, and then per stage every warp
-//                reads rows lane, lane + 32, ... and stores word w of row group
-//                i to column 4 w + i of its own lane quarter, which is the
-//                transposition the layout needs
-//   warps 10-17  epilogue: tensor memory -> registers -> y
-// A stage's barrier counts the four scale warps and the copies' bytes.
+//   next         scales, see below
+//   last 8       epilogue: tensor memory -> registers -> y
+//
+// Scales, stored: two groups of four warps take turns. A group reads the scales
+// of every row for 4 stages (32 bytes of MX4, 64 of NV4) into registers one
+// turn ahead, lays them down row by row in shared memory, and per stage every
+// warp reads rows lane, lane + 32, ... and stores word w of row group i to
+// column 4 w + i of its own lane quarter.
+// Scales, copied (pairs with NV4): two groups of three warps take turns. Warp b
+// has 128 rows (b = 0: of the weights); a lane reads 32 scale bytes (2 stages)
+// of rows lane, lane + 32, + 64, + 96 into registers one turn ahead and per
+// stage stores word w of its four rows as 16 bytes: the 512 bytes that one
+// tcgen05.cp (32 lanes x 16 bytes, to all four lane quarters), issued before
+// the stage's MMAs, takes to columns 4 w .. 4 w + 3.
+// Storing reads every scale four times from shared memory, which the TMA and
+// the MMAs need too; a copy takes the warp of the MMAs and the tensor core
+// about 30 cycles. 21504 x 5376 x 2048 rows (256 x 256 tiles): NV4 142 us
+// stored, 113 copied, MX4 99 either way, but one wave of such tiles, 18944 x
+// 4096 x 256 rows, 16.3 and 17.3 us; 5376 x 8192 x 777 rows (128 x 128 tiles,
+// half the MMA time per copy): NV4 24.0 and 26.3 us, MX4 21.4 and 23.1 us.
+//
+// A stage's barrier counts the scale warps of a group and the codes' bytes.
 //
 // Every wait is bounded; one that gives up leaves NaN in the outputs of the
 // tiles that were not finished.
@@ -38,12 +51,12 @@ namespace tq {
 using namespace f4;
 namespace {
 
-constexpr int kThreads = 576;
 constexpr int kRowsM = 128;         // weight rows per CTA
 constexpr uint32_t kStageRow = kF4StageRow;
 constexpr uint32_t kTmemColumns = 512;
 constexpr uint32_t kSmemLimit = 227u * 1024u;
-constexpr int kScaleWarps = 4, kScaleGroups = 2, kDrainWarps = 8;
+constexpr int kScaleGroups = 2, kDrainWarps = 8;
+constexpr int kScaleWarps = 4;  // of a group, single CTA
 
 template <int FMT, int NT, int CG>
 struct Plan {
@@ -53,17 +66,27 @@ struct Plan {
   static constexpr uint32_t kScaleCols = kWords * (4 + kBCols);
   static constexpr uint32_t kA = kRowsM * kStageRow;
   static constexpr uint32_t kB = (NT / CG) * kStageRow;
-  static constexpr uint32_t kStage = kA + kB;
-  // scale bytes of a row that a group reads at once, four pieces of one load
-  // each where the ring is long enough (see the assertion below), else two
+  // scales by tcgen05.cp, see above
+  static constexpr bool kCopied = CG == 2 && FMT == TQ_FMT_NV4;
+  static constexpr int kScaleBlocks = 1 + (NT + 127) / 128;  // of 128 rows
+  static constexpr int kArrivals = kCopied ? kScaleBlocks : kScaleWarps;
+  static constexpr int kDrainWarp = 2 + kScaleGroups * kArrivals;
+  static constexpr int kThreads = 32 * (kDrainWarp + kDrainWarps);
+  // copied: 32 bytes of a row in turn, in the ring
+  static constexpr uint32_t kS = kCopied ? kScaleBlocks * 128 * kScaleRow : 0;
+  static constexpr uint32_t kStage = kA + kB + kS;
+  // else scale bytes of a row that a group reads at once, four pieces of one
+  // load each where the ring is long enough (see the assertion below), else
+  // two
   static constexpr uint32_t kPiece = FMT == TQ_FMT_NV4 ? 16u : 8u;
   static constexpr uint32_t kUnit =
-      kPiece * (5 * kStage + 2 * (kRowsM + NT) * 4 * kPiece + 3072u <=
-                        kSmemLimit
-                    ? 4u
-                    : 2u);
+      kCopied ? 32u
+              : kPiece * (5 * kStage + 2 * (kRowsM + NT) * 4 * kPiece + 3072u <=
+                                  kSmemLimit
+                              ? 4u
+                              : 2u);
+  static constexpr uint32_t kScales = kCopied ? 0 : (kRowsM + NT) * kUnit;
   static constexpr int kUnitStages = (int)(kUnit / kScaleRow);
-  static constexpr uint32_t kScales = (kRowsM + NT) * kUnit;  // of one group
   static constexpr int kFit =
       (int)((kSmemLimit - 3072u - kScaleGroups * kScales) / kStage);
   static constexpr int kFitT = (int)((kTmemColumns - NT) / kScaleCols);
@@ -77,7 +100,8 @@ struct Plan {
   // offsets from the 1024-byte aligned base
   static constexpr uint32_t kOffB = kStages * kA;
   static constexpr uint32_t kOffS = kOffB + kStages * kB;
-  static constexpr uint32_t kOffBar = kOffS + kScaleGroups * kScales;
+  static constexpr uint32_t kOffBar = kOffS + kStages * kS +
+                                      kScaleGroups * kScales;
   static constexpr uint32_t kSmem = kOffBar + 512 + 1024;
   static_assert(kSmem <= kSmemLimit, "shared memory");
 };
@@ -139,8 +163,18 @@ __device__ __forceinline__ void arrive_leader(uint32_t bar) {
       : "memory");
 }
 
+// The same with release: also what this thread knows to be written to shared
+// memory.
+__device__ __forceinline__ void announce_leader(uint32_t bar) {
+  uint32_t remote;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(remote) : "r"(bar));
+  asm volatile(
+      "mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(remote)
+      : "memory");
+}
+
 template <int FMT, int NT, int CG>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Plan<FMT, NT, CG>::kThreads, 1)
     product_f4_kernel(const __grid_constant__ CUtensorMap tmap_w,
                       const __grid_constant__ CUtensorMap tmap_x,
                       const Args args) {
@@ -163,7 +197,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(ready + 8 * s, kScaleWarps + 1 + (CG == 2 && rank == 0));
+      mbar_init(ready + 8 * s,
+                P::kArrivals + 1 + (CG == 2 && rank == 0));
       mbar_init(empty + 8 * s, 1);
     }
     mbar_init(dfull, 1);
@@ -182,7 +217,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();  // user memory is read and written from here on
   // all columns are this CTA's, so they start at column 0
   constexpr uint32_t kTmem = 0;
-  constexpr uint32_t tmem_scales = kTmem + NT;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -214,9 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < steps && ok; ++i, ++it) {
           ok = mbar_wait(ready + 8 * (it % S), (it / S) & 1u, abort_addr,
                          kWaitLimitNs);
-          tc_fence_after_sync();
-          tc_fence_before_sync();
-          if (ok) arrive_leader(ready + 8 * (it % S));
+          if (ok) announce_leader(ready + 8 * (it % S));
         }
       }
     }
@@ -245,6 +277,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t s1 = (it + 1) % S, ph1 = ((it + 1) / S) & 1u;
           const bool next = mbar_test<CG>(ready + 8 * s1, ph1);
           const uint32_t sa = kTmem + NT + s * P::kScaleCols;
+          if constexpr (P::kCopied) {
+            const uint64_t scales = smem_desc_rows16(base + P::kOffS + s * P::kS);
+  #pragma unroll
+            for (int b = 0; b < P::kScaleBlocks; ++b)
+              copy_scales<CG, P::kWords>(
+                  b == 0 ? sa : sa + P::kWords * 4 + 4 * (b - 1),
+                  b == 0 ? 4 : P::kBCols, scales + b * P::kWords * 32);
+          }
           mma_stage<FMT, CG>(
               kTmem, smem_desc_kmajor_sw128(base + s * P::kA),
               smem_desc_kmajor_sw128(base + P::kOffB + s * P::kB),
@@ -259,141 +299,222 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint32_t j = it > (uint32_t)S ? it - S : 0; j < it; ++j)
         mbar_wait(empty + 8 * (j % S), (j / S) & 1u);
     }
-  } else if (warp < 2 + kScaleWarps * kScaleGroups) {
-    const int turn = (warp - 2) / kScaleWarps;  // this warp's group
-    const int tid = (threadIdx.x - 64) & 127;
-    const uint32_t quarter = (uint32_t)(warp & 3) << 21;  // lane 32 q, bits 16+
-    const int row_bytes = args.k / (FMT == TQ_FMT_MX4 ? 32 : 16);
-    const bool whole = args.k % 256 == 0;
-    const uint32_t buf = base + P::kOffS + turn * P::kScales;
-    const int units = (steps + P::kUnitStages - 1) / P::kUnitStages;
-    // a row's unit is read by kPieces neighbouring threads
-    constexpr int kPieces = (int)(P::kUnit / P::kPiece), kPass = 128 / kPieces;
-    constexpr int kPieceWords = (int)P::kPiece / 4;
-    constexpr int kRowsPer = (kRowsM + NT + kPass - 1) / kPass;
-    const int my_row = tid / kPieces, my_piece = tid % kPieces;
-    uint32_t v[kRowsPer][kPieceWords];
-    // unit `lu` of tile `lt`, into registers; rows past the matrix repeat the
-    // last one (their outputs are not stored)
-    int at_tile = -1;
-    const uint8_t *wrows = nullptr, *xrows = nullptr;
-    int wlast = 0, xlast = 0;
-    auto load = [&](int lt, int lu) {
-      if (lt != at_tile) {
-        at_tile = lt;
-        const int64_t m0 =
-            (int64_t)(lt / args.tiles_n) * (CG * kRowsM) + rank * kRowsM;
-        const int64_t b0 = (int64_t)(lt % args.tiles_n) * NT;
-        const int64_t m = m0 < args.n ? m0 : args.n - 1;
-        wlast = (int)(args.n - 1 - m < kRowsM ? args.n - 1 - m : kRowsM);
-        xlast = (int)(args.batch - 1 - b0 < NT ? args.batch - 1 - b0 : NT);
-        wrows = args.wscales + m * row_bytes;
-        xrows = args.xscales + b0 * row_bytes;
-      }
-      const int off = lu * (int)P::kUnit + (int)P::kPiece * my_piece;
-      auto each = [&](auto read) {
+  } else if (warp < P::kDrainWarp) {
+    if constexpr (P::kCopied) {
+      const int turn = (warp - 2) / P::kScaleBlocks;  // this warp's group
+      const int block = (warp - 2) % P::kScaleBlocks;
+      const int64_t row_bytes = args.k / f4_block(FMT);
+      const bool whole = args.k % 256 == 0;
+      const int units = (steps + P::kUnitStages - 1) / P::kUnitStages;
+      const uint8_t *const scales = block == 0 ? args.wscales : args.xscales;
+      const int64_t last = (block == 0 ? args.n : args.batch) - 1;
+      // unit `lu` of tile `lt`; rows past the matrix repeat the last one (their
+      // outputs are not stored)
+      auto load = [&](int lt, int lu, uint32_t (&v)[4][8]) {
+        const int64_t row0 =
+            block == 0 ? (int64_t)(lt / args.tiles_n) * (CG * kRowsM) +
+                             rank * kRowsM
+                       : (int64_t)(lt % args.tiles_n) * NT + 128 * (block - 1);
+        const int off = 32 * lu, left = (int)row_bytes - off;
 #pragma unroll
-        for (int j = 0; j < kRowsPer; ++j) {
-          const bool of_w = kPass * (j + 1) <= kRowsM;
-          int r = my_row + kPass * j - (of_w ? 0 : kRowsM);
-          r = min(r, of_w ? wlast : xlast);
-          read(v[j], (of_w ? wrows : xrows) + (int64_t)r * row_bytes + off);
+        for (int i = 0; i < 4; ++i) {
+          const int64_t r = row0 + lane + 32 * i;
+          const uint8_t *p = scales + (r < last ? r : last) * row_bytes + off;
+          // rows whose length is a multiple of a stage's scale bytes (k a
+          // multiple of 256) start on such a boundary
+          if (whole)
+            load_unit<P::kWords>(v[i], p, left);
+          else
+            load_unit<0>(v[i], p, left);
         }
       };
-      // rows whose length is a multiple of a piece (k a multiple of 256)
-      // start on its boundary
-      if (whole)
-        each([&](uint32_t (&d)[kPieceWords], const uint8_t *p) {
-          load_piece(d, p, row_bytes - off);
-        });
-      else
-        each([&](uint32_t (&d)[kPieceWords], const uint8_t *p) {
-          load_piece_bytes(d, p, row_bytes - off);
-        });
-    };
-    // (tile, unit) of this group's next turn: every second unit in order
-    int lt = group, lu = turn;
-    auto settle = [&]() {
-      while (lu >= units) {
-        lu -= units;
-        lt += groups;
-      }
-    };
-    settle();
-    if (lt < tiles) load(lt, lu);
-    bool ok = true;
-    while (lt < tiles) {
-      const int u = lu;
-      // stages before this unit
-      const uint32_t first =
-          (uint32_t)((lt - group) / groups) * steps + u * P::kUnitStages;
-      const int count = steps - u * P::kUnitStages < P::kUnitStages
-                            ? steps - u * P::kUnitStages
-                            : P::kUnitStages;
-      bar_sync(1 + turn, 128);  // the group has read its last unit
-#pragma unroll
-      for (int j = 0; j < kRowsPer; ++j) {
-        if (FMT == TQ_FMT_NV4) {  // E4M3 scales are read without their sign
-#pragma unroll
-          for (int w = 0; w < kPieceWords; ++w) v[j][w] &= 0x7F7F7F7Fu;
+      // (tile, unit) of this group's next turn: every second unit in order
+      int lt = group, lu = turn;
+      auto settle = [&]() {
+        while (lu >= units) {
+          lu -= units;
+          lt += groups;
         }
-        if (my_row + kPass * j < kRowsM + NT)
-          store_piece(buf + scale_at<kPieces, P::kPiece>(my_row + kPass * j,
-                                                         my_piece),
-                      v[j]);
-      }
-      bar_sync(1 + turn, 128);
-      lu += kScaleGroups;
+      };
       settle();
-      if (lt < tiles) load(lt, lu);
-#pragma unroll 1
-      for (int i = 0; i < count; ++i) {
-        const uint32_t it = first + i, s = it % S, ph = (it / S) & 1u;
-        // the MMAs that read this slot's scales before are done; after a wait
-        // that gave up, the warps only keep meeting at the barriers above
-        if (ok)
+      uint32_t v[4][8], next[4][8] = {};
+      if (lt < tiles) load(lt, lu, next);
+      bool ok = true;
+      while (lt < tiles && ok) {
+        // stages before this unit
+        const uint32_t first = (uint32_t)((lt - group) / groups) * steps +
+                               lu * P::kUnitStages;
+        const int count = steps - lu * P::kUnitStages;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int w = 0; w < 8; ++w)  // E4M3 scales are read without their sign
+            v[i][w] = FMT == TQ_FMT_NV4 ? next[i][w] & 0x7F7F7F7Fu : next[i][w];
+        lu += kScaleGroups;
+        settle();
+#pragma unroll
+        for (int i = 0; i < P::kUnitStages; ++i) {
+          if (i >= count || !ok) break;
+          const uint32_t it = first + i, s = it % S, ph = (it / S) & 1u;
+          // the MMAs that read this slot's scales before are done
           ok = mbar_wait(empty + 8 * s, ph ^ 1u, abort_addr, kWaitLimitNs);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) continue;
-        tc_fence_after_sync();
-        const uint32_t cols = tmem_scales + s * P::kScaleCols + quarter;
-#pragma unroll
-        for (int r0 = 0; r0 < 4 + (int)P::kBCols; r0 += 4) {
-          uint32_t a[4][4];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            if (32 * (r0 + r) >= kRowsM + NT) {
-              a[r][0] = a[r][1] = a[r][2] = a[r][3] = 0;
-              continue;
-            }
-            const uint32_t at =
-                buf + scale_at<kPieces, P::kPiece>(32 * (r0 + r) + lane, i);
-            if constexpr (P::kWords == 2)
-              asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];"
-                           : "=r"(a[r][0]), "=r"(a[r][1])
-                           : "r"(at)
-                           : "memory");
-            else
-              asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                           : "=r"(a[r][0]), "=r"(a[r][1]), "=r"(a[r][2]),
-                             "=r"(a[r][3])
-                           : "r"(at)
-                           : "memory");
-          }
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          const uint32_t at = base + P::kOffS + s * P::kS +
+                              block * 128 * P::kScaleRow + 16 * lane;
 #pragma unroll
           for (int w = 0; w < P::kWords; ++w)
-            tmem_st4(r0 == 0 ? cols + 4 * w
-                             : cols + P::kWords * 4 + P::kBCols * w + r0 - 4,
-                     a[0][w], a[1][w], a[2][w], a[3][w]);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             at + 512 * w),
+                         "r"(v[0][i * P::kWords + w]),
+                         "r"(v[1][i * P::kWords + w]),
+                         "r"(v[2][i * P::kWords + w]),
+                         "r"(v[3][i * P::kWords + w])
+                         : "memory");
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(ready + 8 * s);
+          // not before the first stage's stores, which would queue up behind
+          if (i == 0 && lt < tiles) load(lt, lu, next);
         }
-        tmem_st_wait();
-        tc_fence_before_sync();
-        if (lane == 0) mbar_arrive(ready + 8 * s);
-        __syncwarp();
+      }
+    } else {
+      const int turn = (warp - 2) / kScaleWarps;  // this warp's group
+      const int tid = (threadIdx.x - 64) & 127;
+      constexpr uint32_t tmem_scales = kTmem + NT;
+      const uint32_t quarter = (uint32_t)(warp & 3) << 21;  // lane 32 q, bits 16+
+      const int row_bytes = args.k / (FMT == TQ_FMT_MX4 ? 32 : 16);
+      const bool whole = args.k % 256 == 0;
+      const uint32_t buf = base + P::kOffS + turn * P::kScales;
+      const int units = (steps + P::kUnitStages - 1) / P::kUnitStages;
+      // a row's unit is read by kPieces neighbouring threads
+      constexpr int kPieces = (int)(P::kUnit / P::kPiece), kPass = 128 / kPieces;
+      constexpr int kPieceWords = (int)P::kPiece / 4;
+      constexpr int kRowsPer = (kRowsM + NT + kPass - 1) / kPass;
+      const int my_row = tid / kPieces, my_piece = tid % kPieces;
+      uint32_t v[kRowsPer][kPieceWords];
+      // unit `lu` of tile `lt`, into registers; rows past the matrix repeat the
+      // last one (their outputs are not stored)
+      int at_tile = -1;
+      const uint8_t *wrows = nullptr, *xrows = nullptr;
+      int wlast = 0, xlast = 0;
+      auto load = [&](int lt, int lu) {
+        if (lt != at_tile) {
+          at_tile = lt;
+          const int64_t m0 =
+              (int64_t)(lt / args.tiles_n) * (CG * kRowsM) + rank * kRowsM;
+          const int64_t b0 = (int64_t)(lt % args.tiles_n) * NT;
+          const int64_t m = m0 < args.n ? m0 : args.n - 1;
+          wlast = (int)(args.n - 1 - m < kRowsM ? args.n - 1 - m : kRowsM);
+          xlast = (int)(args.batch - 1 - b0 < NT ? args.batch - 1 - b0 : NT);
+          wrows = args.wscales + m * row_bytes;
+          xrows = args.xscales + b0 * row_bytes;
+        }
+        const int off = lu * (int)P::kUnit + (int)P::kPiece * my_piece;
+        auto each = [&](auto read) {
+#pragma unroll
+          for (int j = 0; j < kRowsPer; ++j) {
+            const bool of_w = kPass * (j + 1) <= kRowsM;
+            int r = my_row + kPass * j - (of_w ? 0 : kRowsM);
+            r = min(r, of_w ? wlast : xlast);
+            read(v[j], (of_w ? wrows : xrows) + (int64_t)r * row_bytes + off);
+          }
+        };
+        // rows whose length is a multiple of a piece (k a multiple of 256)
+        // start on its boundary
+        if (whole)
+          each([&](uint32_t (&d)[kPieceWords], const uint8_t *p) {
+            load_piece(d, p, row_bytes - off);
+          });
+        else
+          each([&](uint32_t (&d)[kPieceWords], const uint8_t *p) {
+            load_piece_shifted(d, p, row_bytes - off);
+          });
+      };
+      // (tile, unit) of this group's next turn: every second unit in order
+      int lt = group, lu = turn;
+      auto settle = [&]() {
+        while (lu >= units) {
+          lu -= units;
+          lt += groups;
+        }
+      };
+      settle();
+      if (lt < tiles) load(lt, lu);
+      bool ok = true;
+      while (lt < tiles) {
+        const int u = lu;
+        // stages before this unit
+        const uint32_t first =
+            (uint32_t)((lt - group) / groups) * steps + u * P::kUnitStages;
+        const int count = steps - u * P::kUnitStages < P::kUnitStages
+                              ? steps - u * P::kUnitStages
+                              : P::kUnitStages;
+        bar_sync(1 + turn, 128);  // the group has read its last unit
+#pragma unroll
+        for (int j = 0; j < kRowsPer; ++j) {
+          if (FMT == TQ_FMT_NV4) {  // E4M3 scales are read without their sign
+#pragma unroll
+            for (int w = 0; w < kPieceWords; ++w) v[j][w] &= 0x7F7F7F7Fu;
+          }
+          if (my_row + kPass * j < kRowsM + NT)
+            store_piece(buf + scale_at<kPieces, P::kPiece>(my_row + kPass * j,
+                                                           my_piece),
+                        v[j]);
+        }
+        bar_sync(1 + turn, 128);
+        lu += kScaleGroups;
+        settle();
+        if (lt < tiles) load(lt, lu);
+#pragma unroll 1
+        for (int i = 0; i < count; ++i) {
+          const uint32_t it = first + i, s = it % S, ph = (it / S) & 1u;
+          // the MMAs that read this slot's scales before are done; after a wait
+          // that gave up, the warps only keep meeting at the barriers above
+          if (ok)
+            ok = mbar_wait(empty + 8 * s, ph ^ 1u, abort_addr, kWaitLimitNs);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) continue;
+          tc_fence_after_sync();
+          const uint32_t cols = tmem_scales + s * P::kScaleCols + quarter;
+#pragma unroll
+          for (int r0 = 0; r0 < 4 + (int)P::kBCols; r0 += 4) {
+            uint32_t a[4][4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              if (32 * (r0 + r) >= kRowsM + NT) {
+                a[r][0] = a[r][1] = a[r][2] = a[r][3] = 0;
+                continue;
+              }
+              const uint32_t at =
+                  buf + scale_at<kPieces, P::kPiece>(32 * (r0 + r) + lane, i);
+              if constexpr (P::kWords == 2)
+                asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];"
+                             : "=r"(a[r][0]), "=r"(a[r][1])
+                             : "r"(at)
+                             : "memory");
+              else
+                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(a[r][0]), "=r"(a[r][1]), "=r"(a[r][2]),
+                               "=r"(a[r][3])
+                             : "r"(at)
+                             : "memory");
+            }
+#pragma unroll
+            for (int w = 0; w < P::kWords; ++w)
+              tmem_st4(r0 == 0 ? cols + 4 * w
+                               : cols + P::kWords * 4 + P::kBCols * w + r0 - 4,
+                       a[0][w], a[1][w], a[2][w], a[3][w]);
+          }
+          tmem_st_wait();
+          tc_fence_before_sync();
+          if (lane == 0) mbar_arrive(ready + 8 * s);
+          __syncwarp();
+        }
       }
     }
   } else {
-    const int q = warp & 3, half = (warp - 10) >> 2;  // lane quarter, columns
+    const int q = warp & 3, half = (warp - P::kDrainWarp) >> 2;  // lanes, columns
     constexpr int kCols = NT / 2;
     const float g = (args.wg != nullptr ? *args.wg : 1.0f) *
                     (args.xg != nullptr ? *args.xg : 1.0f);
@@ -563,7 +684,7 @@ cudaError_t launch(const WeightsView &w, const WeightsView &x, Args a,
     return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(groups * CG));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(P::kThreads);
   cfg.dynamicSmemBytes = P::kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];

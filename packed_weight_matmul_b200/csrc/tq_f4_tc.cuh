@@ -122,6 +122,38 @@ __device__ __forceinline__ void mma_stage(uint32_t d, uint64_t a, uint64_t b,
 #undef TQ_MMA
 }
 
+// Descriptor of 32 rows x 16 bytes that lie one after another.
+__device__ __forceinline__ uint64_t smem_desc_rows16(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(128u >> 4) << 16) |
+         ((uint64_t)(128u >> 4) << 32) | (1ull << 46);
+}
+
+// WORDS times 512 bytes of shared memory (of each CTA of a pair), described by
+// `src` and following one another, to tensor-memory columns t, t + step, ...:
+// 16 bytes of lane r to 4 columns of lanes r, r + 32, r + 64, r + 96. Ordered
+// before the MMAs that the elected lane issues later. Whole warp.
+template <int CG, int WORDS>
+__device__ __forceinline__ void copy_scales(uint32_t t, uint32_t step,
+                                            uint64_t src) {
+#define TQ_CP(GROUP)                                                          \
+  asm volatile(                                                               \
+      "{\n .reg .pred q;\n .reg .b64 s1;\n elect.sync _|q, 0xFFFFFFFF;\n"     \
+      " add.s64 s1, %2, 32;\n"                                                \
+      " @q tcgen05.cp.cta_group::" GROUP ".32x128b.warpx4 [%0], %2;\n"        \
+      " @q tcgen05.cp.cta_group::" GROUP ".32x128b.warpx4 [%1], s1;\n}" ::"r"(  \
+          t + 2 * i * step),                                                  \
+      "r"(t + (2 * i + 1) * step), "l"(src + 64 * i)                          \
+      : "memory")
+#pragma unroll
+  for (uint32_t i = 0; i < WORDS / 2; ++i) {
+    if constexpr (CG == 1)
+      TQ_CP("1");
+    else
+      TQ_CP("2");
+  }
+#undef TQ_CP
+}
+
 // Instruction descriptor of the 4-bit kinds: scale byte of B at bits 4-5 and
 // of A at 29-30 (first of the word's bytes that this MMA uses), E2M1 = 1 at
 // 7-9 and 10-12, N >> 3 at 17-22, E8M0 scales at 23, M >> 4 at 24-28.
@@ -157,17 +189,42 @@ __device__ __forceinline__ void load_piece(uint32_t (&v)[WORDS],
   }
 }
 
-// The same byte by byte, for rows that do not start on a piece's boundary.
+// The same for any p, by the aligned words that hold the bytes; a word without
+// any of them is not read.
 template <int WORDS>
-__device__ __forceinline__ void load_piece_bytes(uint32_t (&v)[WORDS],
-                                                 const uint8_t *p, int left) {
+__device__ __forceinline__ void load_piece_shifted(uint32_t (&v)[WORDS],
+                                                   const uint8_t *p, int left) {
+  const int skip = (int)(reinterpret_cast<uintptr_t>(p) & 3u);
+  const uint32_t *q = reinterpret_cast<const uint32_t *>(p - skip);
+  uint32_t x[WORDS + 1];
+#pragma unroll
+  for (int w = 0; w <= WORDS; ++w) {
+    x[w] = 0;
+    if (4 * w < left + skip && (w < WORDS || skip != 0)) x[w] = __ldg(q + w);
+  }
 #pragma unroll
   for (int w = 0; w < WORDS; ++w) {
-    uint32_t x = 0;
-#pragma unroll 1
-    for (int b = 0; b < 4 && 4 * w + b < left; ++b)
-      x |= (uint32_t)__ldg(p + 4 * w + b) << (8 * b);
-    v[w] = x;
+    const uint32_t u = __funnelshift_r(x[w], x[w + 1], 8 * skip);
+    const int n = left - 4 * w;  // bytes of the row in this word
+    v[w] = n >= 4 ? u : n <= 0 ? 0u : u & ((1u << (8 * n)) - 1u);
+  }
+}
+
+// 32 scale bytes of a row: in pieces of WORDS words to whose size `p` is
+// aligned, or of any alignment (WORDS = 0).
+template <int WORDS>
+__device__ __forceinline__ void load_unit(uint32_t (&v)[8], const uint8_t *p,
+                                          int left) {
+  if constexpr (WORDS == 0) {
+    load_piece_shifted(v, p, left);
+  } else {
+#pragma unroll
+    for (int c = 0; c < 8 / WORDS; ++c) {
+      uint32_t d[WORDS];
+      load_piece(d, p + 4 * WORDS * c, left - 4 * WORDS * c);
+#pragma unroll
+      for (int w = 0; w < WORDS; ++w) v[c * WORDS + w] = d[w];
+    }
   }
 }
 
