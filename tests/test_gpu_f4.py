@@ -235,6 +235,21 @@ def test_linear_exact(fmt, n, k):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("n,k,b", [(130, 288, 33), (257, 544, 64),
+                                   (64, 2080, 65), (1003, 4128, 130)])
+def test_linear_without_workspace(fmt, n, k, b):
+    """Batches for which a workspace would help."""
+    codes, scales = exact_package(fmt, n, k, n + k)
+    w, x = weights(fmt, F.pack(codes), scales, None), integers(b, k, b)
+    y = torch.full((b, n), float("nan"), device=U.DEV)
+    assert U.tq().lib().tq_linear(w.desc, x.data_ptr(), b, k, y.data_ptr(), n,
+                                  None) == U.tq().TQ_OK
+    torch.cuda.synchronize()
+    assert torch.equal(y.double(),
+                       x.double() @ F.values(codes, scales, fmt).t())
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("n,k,b", [(300, 1024, 1), (300, 1056, 7),
                                    (1000, 5376, 16), (520, 8192, 40),
                                    (200, 21504, 64), (96, 21504, 3)])
@@ -405,11 +420,12 @@ def linear_ws(w, x, used=True):
 
 
 # n, k, batches: many weights from 3 rows on (NV4: n >= k), fewer weights from
-# 32 rows on; ragged tiles, a last stage of 32 to 160 codes, several chunks of
+# 33 rows on; ragged tiles, a last stage of 32 to 160 codes, several chunks of
 # 512 rows
 DIGITS = [(MX4, 4096, 8192, (3, 5, 8, 9, 20)), (MX4, 1003, 33472, (4, 7)),
           (NV4, 8200, 4128, (3, 8, 13, 33)), (NV4, 5800, 5792, (5, 17)),
-          (MX4, 1040, 2080, (32, 33, 65, 130)), (NV4, 1040, 2080, (32, 64, 97)),
+          (MX4, 1040, 2080, (33, 65, 130)), (NV4, 1040, 2080, (40, 64, 97)),
+          (MX4, 3, 32, (33, 200)), (NV4, 130, 96, (36, 64)),
           (MX4, 1100, 1952, (600, 1030)), (NV4, 1100, 1952, (513,))]
 
 
@@ -419,19 +435,20 @@ def test_digit_rows_exact(fmt, n, k, batches):
     codes, scales = exact_package(fmt, n, k, n + k)
     if k > 20000:  # partial sums below 2^22 in steps of 1/4
         codes &= 11
-    codes[:, 100] = 2  # no 0 * Inf in the checked column
-    codes[3] = 0
-    codes[3, 100] = 1
-    scales[n - 2, 1] = 255 if fmt == MX4 else 127
+    col = min(100, k - 1)
+    codes[:, col] = 2  # no 0 * Inf in the checked column
+    codes[n // 2] = 0
+    codes[n // 2, col] = 1
+    scales[n - 2, -1] = 255 if fmt == MX4 else 127
     w64 = F.values(codes, scales, fmt)
     w = weights(fmt, F.pack(codes), scales, None)
     for b in batches:
         x = integers(b, k, b)
         x[b // 2] = 0
-        x[1, 100] = float("inf")
+        x[1, col] = float("inf")
         if b > 3:
             x[2, 31] = float("nan")
-            x[3, 100] = -float("inf")
+            x[3, col] = -float("inf")
         ref = x.double() @ w64.t()
         y = linear_ws(w, x)
         nan = torch.isnan(ref)
