@@ -252,16 +252,17 @@ tq_status tq_linear_ws(const tq_weights *w, const void *x_bf16, int64_t batch,
                                        (size_t)v.n * sizeof(float),
                                        (size_t)batch, stream));
   }
-  if (workspace != nullptr && tq::is_f4(v.format)) {
-    const int64_t need = tq::digits_f4_workspace(v, batch);
+  const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(x_bf16);
+  if (tq::is_f4(v.format)) {
+    const int64_t need =
+        workspace != nullptr ? tq::digits_f4_workspace(v, batch) : 0;
     if (need > 0 && (uint64_t)need <= workspace_bytes)
-      return from_cuda(tq::digits_f4(
-          v, static_cast<const __nv_bfloat16 *>(x_bf16), batch, ldx, y, ldy,
-          static_cast<uint8_t *>(workspace), stream));
+      return from_cuda(tq::digits_f4(v, x, batch, ldx, y, ldy,
+                                     static_cast<uint8_t *>(workspace),
+                                     stream));
+    return from_cuda(tq::linear_f4_bf16(v, x, batch, ldx, y, ldy, stream));
   }
-  return from_cuda(tq::launch_linear(
-      v, static_cast<const __nv_bfloat16 *>(x_bf16), batch, ldx, y, ldy,
-      stream));
+  return from_cuda(tq::launch_linear(v, x, batch, ldx, y, ldy, stream));
 }
 
 tq_status tq_linear_f4(const tq_weights *w, const tq_weights *x, void *y,

@@ -1,5 +1,4 @@
 // Dispatch of tq_linear to the fused matmul kernels.
-#include "tq_f4.cuh"
 #include "tq_linear.cuh"
 
 namespace tq {
@@ -9,7 +8,6 @@ std::atomic<int> g_test_force_path{0};
 cudaError_t launch_linear(const WeightsView &w, const __nv_bfloat16 *x,
                           int64_t batch, int64_t ldx, float *y, int64_t ldy,
                           cudaStream_t stream) {
-  if (is_f4(w.format)) return linear_f4_bf16(w, x, batch, ldx, y, ldy, stream);
   const int force = g_test_force_path.load();
   if ((force == 2 || force == 3) && gemm_tc_supported(w, batch))
     return gemm_tc(w, x, batch, ldx, y, ldy, stream);
