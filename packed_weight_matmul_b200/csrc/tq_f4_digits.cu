@@ -111,18 +111,19 @@ __global__ void __launch_bounds__(256)
 //   MX4  21504 x 5376 batch 4: 23, 16.5; 16: 43, 23; 64: 113, 40
 //        5376 x 21504 batch 4: 28, 20; 8192 x 5376 batch 4: 13.5, 11
 //        4096 x 4096 batch 8: 6.7, 11; 32: 12.7, 11.7; 48: 17.8, 11.9
-//        1000 x 4000 batch 32: 10.2, 13.0; 48: 15.3, 13.0
-//        128 x 512 batch 33: 11.4, 6.4; 300 x 12000 batch 48: 29.4, 27.5
 //   NV4  21504 x 5376 batch 4: 29, 20; 16: 42, 28; 64: 107, 56
 //        5376 x 21504 batch 4: 22.6, 24; 16: 31, 37; 64: 76, 66
 //        4096 x 4096 batch 32: 12.4, 12.2; 48: 17.3, 12.5
-// The second launch costs 4 us, the plain kernel grows by half past 32 rows, and long rows of x cost more digits for the
-// same weights, which the larger part of NV4 shows.
+//        1000 x 4000 batch 64: 9.3, 14.5; 130: 19.6, 15.9
+//        128 x 512 batch 64: 4.2, 6.6; 300: 4.5, 7.2
+// The second launch costs 4 us, and long rows of x cost more digits for the
+// same weights, which the larger part of NV4 shows. The plain kernel slows down
+// past 32 rows unless it has room for passes of 8 or 16 next to one another.
 int64_t digits_f4_workspace(const WeightsView &w, int64_t batch) {
   const int64_t weights = w.n * w.k;
   const bool large = batch >= 3 && weights >= (1 << 25) &&
                      (w.format == TQ_FMT_MX4 || w.n >= w.k);
-  const bool wide = batch > 32;
+  const bool wide = batch > 32 && rows_per_pass_f4(w, 1, batch) > 16;
   if (!(large || wide) || !decode_f4_supported(w, 1)) return 0;
   return layout_of(w.format, batch, w.k).total;
 }

@@ -43,6 +43,7 @@ constexpr int kStageK = 256;    // codes of a row per stage
 constexpr int kSegment = 1024;  // ids looked through at once
 constexpr int kList = 2 * kSegment;  // rows of an expert gathered for its passes
 constexpr int kPrefetch = 1024; // bytes of a row hinted to the L2 cache
+constexpr int kPlaces = 2 * 148;  // CTAs that run at once
 
 struct RowArgs {
   const uint8_t *codes, *scales;  // weights (of expert 0)
@@ -610,7 +611,7 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
       const uint32_t vote = __ballot_sync(0xFFFFFFFFu, is);
       if (lane == 0) s_count[j * kWarps + warp] = __popc(vote);
       if (is) hit |= 1u << j;
-      if (expert == 0 && rank == 0 && i < a.batch &&
+      if (expert == 0 && rank == 0 && blockIdx.z == 0 && i < a.batch &&
           (id < 0 || id >= a.n_experts)) {
         // nobody's row: NaN in this CTA's columns
         const int64_t end = row0 + kTile < a.n ? row0 + kTile : a.n;
@@ -656,7 +657,8 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
     __syncthreads();
     held += s_count[kSegment / 32];
     if (held > kList - kSegment || seg + kSegment >= a.batch) {
-      for (int base = 0; base < held; base += NT) {
+      // (the passes of an expert are shared by the CTAs along z)
+      for (int base = NT * blockIdx.z; base < held; base += NT * gridDim.z) {
         pass(base, 0, held - base < NT ? held - base : NT, started);
         started = false;
       }
@@ -685,8 +687,8 @@ int resident(int ks, int dev) {
 
 // `copies`: how many row products of n rows run at once (passes, experts).
 template <int FMT, int NT, bool WHOLE>
-cudaError_t launch_whole(RowArgs a, int64_t copies, int64_t grid_y,
-                   cudaStream_t stream) {
+cudaError_t launch_whole(RowArgs a, int64_t copies, dim3 grid,
+                         cudaStream_t stream) {
   using P = RowPlan<FMT, NT>;
   auto kern = rows_f4_kernel<FMT, NT, WHOLE>;
   cudaError_t e =
@@ -707,7 +709,7 @@ cudaError_t launch_whole(RowArgs a, int64_t copies, int64_t grid_y,
       break;
     }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * a.ks), (unsigned)grid_y);
+  cfg.gridDim = dim3((unsigned)(tiles * a.ks), grid.y, grid.z);
   cfg.blockDim = dim3(P::kThreads);
   cfg.dynamicSmemBytes = P::kSmem;
   cfg.stream = stream;
@@ -724,33 +726,29 @@ cudaError_t launch_whole(RowArgs a, int64_t copies, int64_t grid_y,
 }
 
 template <int FMT, int NT>
-cudaError_t launch(const RowArgs &a, int64_t copies, int64_t grid_y,
+cudaError_t launch(const RowArgs &a, int64_t copies, dim3 grid,
                    cudaStream_t stream) {
   return a.k % kStageK == 0
-             ? launch_whole<FMT, NT, true>(a, copies, grid_y, stream)
-             : launch_whole<FMT, NT, false>(a, copies, grid_y, stream);
+             ? launch_whole<FMT, NT, true>(a, copies, grid, stream)
+             : launch_whole<FMT, NT, false>(a, copies, grid, stream);
 }
 
 template <int NT>
 cudaError_t launch_format(int format, const RowArgs &a, int64_t copies,
-                          int64_t grid_y, cudaStream_t stream) {
+                          dim3 grid, cudaStream_t stream) {
   return format == TQ_FMT_MX4
-             ? launch<TQ_FMT_MX4, NT>(a, copies, grid_y, stream)
-             : launch<TQ_FMT_NV4, NT>(a, copies, grid_y, stream);
+             ? launch<TQ_FMT_MX4, NT>(a, copies, grid, stream)
+             : launch<TQ_FMT_NV4, NT>(a, copies, grid, stream);
 }
 
 cudaError_t launch_nt(int format, int nt, const RowArgs &a, int64_t copies,
-                      int64_t grid_y, cudaStream_t stream) {
+                      dim3 grid, cudaStream_t stream) {
   switch (nt) {
-    case 8: return launch_format<8>(format, a, copies, grid_y, stream);
-    case 16: return launch_format<16>(format, a, copies, grid_y, stream);
-    case 32: return launch_format<32>(format, a, copies, grid_y, stream);
-    default: return launch_format<64>(format, a, copies, grid_y, stream);
+    case 8: return launch_format<8>(format, a, copies, grid, stream);
+    case 16: return launch_format<16>(format, a, copies, grid, stream);
+    case 32: return launch_format<32>(format, a, copies, grid, stream);
+    default: return launch_format<64>(format, a, copies, grid, stream);
   }
-}
-
-int rows_per_pass(int64_t rows) {
-  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
 
 RowArgs weight_args(const WeightsView &w) {
@@ -764,6 +762,15 @@ RowArgs weight_args(const WeightsView &w) {
 }
 
 }  // namespace
+
+int rows_per_pass_f4(const WeightsView &w, int64_t copies, int64_t rows) {
+  int nt = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  const int64_t tiles = (w.n + 127) / 128;
+  const int64_t split = (w.k + kStageK - 1) / kStageK / 2;  // of K, at most
+  const int64_t each = tiles * copies * (split < 1 ? 1 : split < 8 ? split : 8);
+  while (nt > 8 && each * ((rows + nt / 2 - 1) / (nt / 2)) <= kPlaces) nt /= 2;
+  return nt;
+}
 
 cudaError_t linear_f4_bf16(const WeightsView &w, const __nv_bfloat16 *x,
                            int64_t batch, int64_t ldx, float *y, int64_t ldy,
@@ -780,7 +787,7 @@ cudaError_t linear_f4_bf16(const WeightsView &w, const __nv_bfloat16 *x,
   a.batch = batch;
   a.y = y;
   a.ldy = ldy;
-  const int nt = rows_per_pass(batch);
+  const int nt = rows_per_pass_f4(w, 1, batch);
   const int64_t passes = (batch + nt - 1) / nt;
   cudaError_t e = cudaSuccess;
   // a grid's second dimension ends at 65535
@@ -790,7 +797,7 @@ cudaError_t linear_f4_bf16(const WeightsView &w, const __nv_bfloat16 *x,
     b.x += p * nt * ldx;
     b.y = y + p * nt * ldy;
     b.batch -= p * nt;
-    e = launch_nt(w.format, nt, b, now, now, stream);
+    e = launch_nt(w.format, nt, b, now, dim3(1, (unsigned)now), stream);
   }
   return e;
 }
@@ -821,8 +828,18 @@ cudaError_t launch_linear_experts_f4(const WeightsView &w, int n_experts,
   // all tiles run at once and one expert's second pass is the tail (32 experts
   // of 1024 x 4096 at 256 rows: 48 us against 55 us).
   const int64_t used = tokens < n_experts ? tokens : n_experts;
-  const int nt = rows_per_pass(2 * ((tokens + n_experts - 1) / n_experts));
-  return launch_nt(w.format, nt, a, used, n_experts, stream);
+  const int64_t most = 2 * ((tokens + n_experts - 1) / n_experts);
+  const int nt = rows_per_pass_f4(w, used, most);
+  // CTAs that share an expert's passes: all of twice the mean where the passes
+  // were cut for it, else what the mean needs (768 x 2048, 8 experts, 300 rows:
+  // 19 us, with one for each pass of twice the mean 28 us).
+  const int64_t room = kPlaces / (used * ((w.n + 127) / 128));
+  int64_t z = nt < 64 && nt < most / 2 ? (most + nt - 1) / nt
+                                       : (most / 2 + nt - 1) / nt;
+  z = z < room ? z : room;
+  z = z < 1 ? 1 : z;
+  return launch_nt(w.format, nt, a, used * z,
+                   dim3(1, (unsigned)n_experts, (unsigned)z), stream);
 }
 
 }  // namespace tq

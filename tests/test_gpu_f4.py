@@ -419,13 +419,13 @@ def linear_ws(w, x, used=True):
     return y
 
 
-# n, k, batches: many weights from 3 rows on (NV4: n >= k), fewer weights from
-# 33 rows on; ragged tiles, a last stage of 32 to 160 codes, several chunks of
+# n, k, batches: many weights from 3 rows on (NV4: n >= k), fewer weights past
+# 32 rows; ragged tiles, a last stage of 32 to 160 codes, several chunks of
 # 512 rows
 DIGITS = [(MX4, 4096, 8192, (3, 5, 8, 9, 20)), (MX4, 1003, 33472, (4, 7)),
           (NV4, 8200, 4128, (3, 8, 13, 33)), (NV4, 5800, 5792, (5, 17)),
-          (MX4, 1040, 2080, (33, 65, 130)), (NV4, 1040, 2080, (40, 64, 97)),
-          (MX4, 3, 32, (33, 200)), (NV4, 130, 96, (36, 64)),
+          (MX4, 2080, 4128, (33, 65, 130)), (NV4, 2080, 4128, (40, 64, 97)),
+          (MX4, 70, 32, (9500,)),
           (MX4, 1100, 1952, (600, 1030)), (NV4, 1100, 1952, (513,))]
 
 
@@ -459,7 +459,7 @@ def test_digit_rows_exact(fmt, n, k, batches):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
-@pytest.mark.parametrize("n,k,b", [(8192, 4096, 6), (1040, 2080, 40),
+@pytest.mark.parametrize("n,k,b", [(8192, 4096, 6), (2080, 4128, 40),
                                    (1100, 1952, 515)])
 def test_digit_rows_range(fmt, n, k, b):
     """x over many powers of two inside a row, rows at both ends of the
@@ -485,16 +485,16 @@ def test_digit_rows_range(fmt, n, k, b):
 def test_digit_rows_small_workspace():
     """One byte too few: the plain kernels, the workspace untouched."""
     tq = U.tq()
-    codes, scales = exact_package(MX4, 1040, 2080, 1)
+    codes, scales = exact_package(MX4, 2080, 4128, 1)
     w = weights(MX4, F.pack(codes), scales)
-    x = integers(40, 2080, 2)
+    x = integers(40, 4128, 2)
     need = tq.lib().tq_linear_workspace(w.desc, 40)
     ws = torch.full((need,), 0xFF, dtype=torch.uint8, device=U.DEV)
-    y = torch.full((40, 1040), float("nan"), device=U.DEV)
+    y = torch.full((40, 2080), float("nan"), device=U.DEV)
     for ptr, size in ((ws.data_ptr(), need - 1), (None, 0), (None, need)):
         y.fill_(float("nan"))
-        assert tq.lib().tq_linear_ws(w.desc, x.data_ptr(), 40, 2080,
-                                     y.data_ptr(), 1040, ptr, size,
+        assert tq.lib().tq_linear_ws(w.desc, x.data_ptr(), 40, 4128,
+                                     y.data_ptr(), 2080, ptr, size,
                                      None) == tq.TQ_OK
         torch.cuda.synchronize()
         assert torch.equal(y.double(),
@@ -506,11 +506,11 @@ def test_digit_rows_streams_and_graphs():
     """Two streams at once, and two captured graphs replayed in turn, each
     with scratch of its own."""
     tq = U.tq()
-    codes, scales = exact_package(NV4, 1040, 2080, 5)
+    codes, scales = exact_package(NV4, 2080, 4128, 5)
     w64 = F.values(codes, scales, NV4)
     w = weights(NV4, F.pack(codes), scales)
-    xs = [integers(b, 2080, b) for b in (40, 70)]
-    ys = [torch.zeros(x.shape[0], 1040, device=U.DEV) for x in xs]
+    xs = [integers(b, 4128, b) for b in (40, 70)]
+    ys = [torch.zeros(x.shape[0], 2080, device=U.DEV) for x in xs]
     refs = [x.double() @ w64.t() for x in xs]
     sides = [torch.cuda.Stream(), torch.cuda.Stream()]
     torch.cuda.synchronize()
