@@ -149,7 +149,9 @@ typedef struct {
 /* TQ_FMT_MX4 / TQ_FMT_NV4 descriptors: codes and scales as laid out above
  * (scales is a byte pointer stored in this field), both 16-byte aligned;
  * lut = the device tensor scale g (NV4, 4-byte aligned) or NULL; planes 1;
- * group 0 or the block size; k_cols % 32 == 0; every other field 0. */
+ * group 0 or the block size; k_cols % 32 == 0; every other field 0. Kernels
+ * read scales in aligned 4-byte words, so up to 3 bytes beside the package may
+ * be read too (never across a page); they are ignored. */
 
 /* Bytes of a package: A = planes * n * (k/G) * (ceil(G/5) + 2) (codes and
  * scales; "Count the bytes you actually wrote"), B = n * k + 972 (codes and

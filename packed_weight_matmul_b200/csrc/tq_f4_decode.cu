@@ -6,15 +6,17 @@
 // The codes of 128 weight rows go from global to shared memory by TMA as they
 // lie, their scales to tensor memory, and tcgen05.mma (kind mxf4 / mxf4nvf4)
 // multiplies them by a 4-bit x. Packed x (tq_linear_f4) is such a matrix
-// already. A bf16 x is written as a sum of 8 of them, exactly enough:
-//
-//   (tq_f4_digits.cuh: base-8 digits, row 8 b + i of the B operand holds digit
-//   i of row b of x).
+// already. A bf16 x is written as a sum of 8 of them, exactly enough
+// (tq_f4_digits.cuh: base-8 digits, row 8 b + i of the B operand holds digit i
+// of row b of x).
 //
 // Bound by the codes' way from HBM: an MMA of 64 k takes 41 to 64 cycles for
 // 8192 weights, 2 to 3 times the rate at which HBM delivers them. A digit
 // costs 3 lane instructions per value of x and CTA, so the kernel takes 16
-// rows of x at most.
+// rows of x at most. MX4, 8192 x 5376: 1 row 10.0 us, 16 packed rows 8.9 us
+// (HBM alone 3.6; 5 us are start-up and the sum over the cluster); 21504 x
+// 5376, 1 row: 16.5 us, 3.7 TB/s; 64 rows over 128 experts of 768 x 2048: 18
+// us.
 //
 // One CTA per 128 weight rows and slice of K, two CTAs per SM (one starts up
 // or ends while the other streams), the slices of a tile in a cluster that

@@ -4,8 +4,10 @@
 //
 // for bf16 x (tq_linear) and for rows of x that pick their matrix
 // (tq_linear_experts_f4).
-// Bound by the codes' way from HBM (0.53 bytes per weight), so a weight may
-// cost about 3 lane instructions.
+// Meant to be bound by the codes' way from HBM (0.53 bytes per weight), which
+// leaves about 3 lane instructions for a weight; at 2.3 (counted) issue slots
+// and start-up bind first. NV4, 5376 x 21504, 4 rows: 22.3 us, 2.9 TB/s; 128
+// experts of 768 x 2048, 500 rows: 42 to 46 us; 1003 x 4128, 13 rows: 8.2 us.
 //
 // Arithmetic. Codes become fp16 pairs by one conversion instruction each, are
 // multiplied by their block's scale in fp16 (exact, see below) and go as the

@@ -336,9 +336,18 @@ def weights_b(codes, lut, rho=None, rows_per_scale=0, n=None, k=None,
     return Weights(d, (codes, lut, rho))
 
 
+def _f4_stacked(fmt, codes, scales, lut, count, n, k, what):
+    """Whether the tensors hold `count` matrices of n x k."""
+    if codes.numel() * 2 < count * n * k or \
+            scales.numel() * F4_BLOCK[fmt] < count * n * k or \
+            (lut is not None and lut.numel() < count):
+        raise TqError(TQ_ERR_SHAPE, f"{what}: fewer than {count} x {n} x {k}")
+
+
 def _weights_f4(fmt, codes, scales, lut, n, k) -> Weights:
     if n is None:
         n, k = codes.shape[0], codes.shape[1] * 2
+    _f4_stacked(fmt, codes, scales, lut, 1, n, k, "weights")
     d = tq_weights(format=fmt, group=F4_BLOCK[fmt], planes=1,
                    rows_per_scale=0, n_rows=n, k_cols=k, codes=_ptr(codes),
                    scales=_ptr(scales), lut=_ptr(lut), codes_plane_stride=0,
@@ -495,6 +504,11 @@ def tq_linear_experts_f4(w: Weights, n_experts, ids, x, y, status=None,
     _f4_tensor(ids, (torch.int32,), "tq_linear_experts_f4: ids")
     _f4_tensor(x, (torch.bfloat16,), "tq_linear_experts_f4: x")
     _f4_tensor(y, (torch.float32,), "tq_linear_experts_f4: y")
+    if ids.dim() != 1 or x.dim() != 2 or y.dim() != 2:
+        raise TqError(TQ_ERR_SHAPE, "tq_linear_experts_f4: ids, x, y")
+    if w.desc.format in F4_BLOCK:
+        _f4_stacked(w.desc.format, *w._keep, n_experts, w.n, w.k,
+                    "tq_linear_experts_f4")
     t = ids.shape[0]
     if x.shape[0] < t or y.shape[0] < t or x.shape[1] < w.k or \
             y.shape[1] < w.n:

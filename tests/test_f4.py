@@ -227,6 +227,20 @@ def test_experts_refusals(tq):
     assert call(t=0, ids=None, x=None, y=None) == tq.TQ_OK
 
 
+def test_binding_refuses_short_packages(tq):
+    c, s = torch.zeros(6, 16, dtype=torch.uint8), torch.zeros(
+        6, 2, dtype=torch.uint8)
+    g = torch.ones(3)
+    assert tq.weights_nv4(c, s, g, 2, 32).n == 2  # three experts
+    for args in ((c, s, g, 7, 32), (c, s[:5], None), (c[:, :8], s, g, 6, 32),
+                 (c, s, torch.ones(0))):
+        with pytest.raises(tq.TqError) as e:
+            tq.weights_nv4(*args)
+        assert e.value.status == tq.TQ_ERR_SHAPE
+    with pytest.raises(tq.TqError):
+        tq.weights_mx4(c, s[:, :0])
+
+
 def test_binding_refuses_host_tensors(tq):
     W = torch.zeros(2, 32, dtype=torch.bfloat16)
     c, s = torch.zeros(2, 16, dtype=torch.uint8), torch.zeros(

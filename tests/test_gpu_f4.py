@@ -625,6 +625,24 @@ def test_experts_invalid_ids(fmt):
     assert run_experts(fmt, 2, 20, 64, [5, 9], 3) == U.tq().TQ_ERR_INVALID_ARG
 
 
+def test_experts_binding_refusals():
+    tq = U.tq()
+    codes, scales = exact_package(NV4, 3 * 8, 64, 1)
+    g = torch.ones(3, device=U.DEV)
+    w = weights(NV4, F.pack(codes), scales, g, 8, 64)
+    ids = torch.zeros(4, dtype=torch.int32, device=U.DEV)
+    x, y = integers(4, 64, 2), torch.zeros(4, 8, device=U.DEV)
+    tq.tq_linear_experts_f4(w, 3, ids, x, y)
+    short = weights(NV4, F.pack(codes), scales, g[:2], 8, 64)
+    for args in ((w, 4, ids, x, y), (short, 3, ids, x, y),
+                 (w, 3, ids.view(2, 2), x, y), (w, 3, ids.long(), x, y),
+                 (w, 3, ids, x[:3], y), (w, 3, ids, x, y[:, :7]),
+                 (w, 3, ids, x[:, ::2], y), (w, 3, ids, x.float(), y)):
+        with pytest.raises(tq.TqError):
+            tq.tq_linear_experts_f4(*args)
+    torch.cuda.synchronize()
+
+
 # ---- in a row -----------------------------------------------------------------------
 
 @pytest.mark.parametrize("fmt", FMTS)
