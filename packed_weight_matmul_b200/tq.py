@@ -436,15 +436,23 @@ def tq_linear(w: Weights, x, y, batch=None, ldx=None, ldy=None, stream=None,
     return st
 
 
-def _f4_tensor(t, dtypes, what):
+def _f4_device(t, what):
+    """The current device, on which t has to lie."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise TqError(TQ_ERR_INVALID_ARG, f"{what}: not on the current device")
+    return dev
+
+
+def _f4_tensor(t, dtypes, dev, what):
     """The 4-bit entry points check what the C ABI cannot see of a tensor:
     that it lies on the current device, with the element type it is read as
     and dense rows."""
-    if not t.is_cuda or t.get_device() != torch._C._cuda_getDevice():
+    if t.get_device() != dev:
         raise TqError(TQ_ERR_INVALID_ARG, f"{what}: not on the current device")
     if t.dtype not in dtypes:
         raise TqError(TQ_ERR_INVALID_ARG, f"{what}: {t.dtype}")
-    if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
+    if not t.is_contiguous() and t.stride(-1) != 1 and t.shape[-1] > 1:
         raise TqError(TQ_ERR_INVALID_ARG, f"{what}: rows are not dense")
 
 
@@ -465,15 +473,16 @@ def tq_quantize_f4(W, fmt, codes_out, scales_out, tensor_scale=None,
     [n][k/16] (TQ_FMT_NV4). NV4: tensor_scale is read when scale_given, else
     written."""
     n, k = W.shape
-    _f4_tensor(W, _BF16, "tq_quantize_f4: W")
-    _f4_tensor(codes_out, _U8, "tq_quantize_f4: codes_out")
-    _f4_tensor(scales_out, _U8, "tq_quantize_f4: scales_out")
+    dev = _f4_device(W, "tq_quantize_f4: W")
+    _f4_tensor(W, _BF16, dev, "tq_quantize_f4: W")
+    _f4_tensor(codes_out, _U8, dev, "tq_quantize_f4: codes_out")
+    _f4_tensor(scales_out, _U8, dev, "tq_quantize_f4: scales_out")
     if codes_out.numel() * 2 < n * k or not codes_out.is_contiguous() or \
             scales_out.numel() * F4_BLOCK.get(fmt, 16) < n * k or \
             not scales_out.is_contiguous():
         raise TqError(TQ_ERR_SHAPE, "tq_quantize_f4: outputs")
     if tensor_scale is not None:
-        _f4_tensor(tensor_scale, _F32, "tq_quantize_f4: scale")
+        _f4_tensor(tensor_scale, _F32, dev, "tq_quantize_f4: scale")
     st = _lib.tq_quantize_f4(W.data_ptr(), n, k, _rows(W), fmt,
                              codes_out.data_ptr(), scales_out.data_ptr(),
                              _ptr(tensor_scale), int(bool(scale_given)),
@@ -486,7 +495,8 @@ def tq_quantize_f4(W, fmt, codes_out, scales_out, tensor_scale=None,
 def tq_linear_f4(w: Weights, x: Weights, y, stream=None, check=True):
     """y = x W^T of two 4-bit matrices of one format; y fp32 or bf16
     [batch][n], row stride free."""
-    _f4_tensor(y, (torch.float32, torch.bfloat16), "tq_linear_f4: y")
+    _f4_tensor(y, _BF16 + _F32, _f4_device(y, "tq_linear_f4: y"),
+               "tq_linear_f4: y")
     if y.dim() != 2 or y.shape[0] < x.n or y.shape[1] < w.n:
         raise TqError(TQ_ERR_SHAPE, "tq_linear_f4: y")
     st = _lib.tq_linear_f4(C.byref(w.desc), C.byref(x.desc), y.data_ptr(),
@@ -501,9 +511,10 @@ def tq_linear_experts_f4(w: Weights, n_experts, ids, x, y, status=None,
                          stream=None, check=True):
     """y[t] = x[t] W_e^T with e = ids[t] (int32, device); w holds the stacked
     experts, w.n the rows of one."""
-    _f4_tensor(ids, (torch.int32,), "tq_linear_experts_f4: ids")
-    _f4_tensor(x, (torch.bfloat16,), "tq_linear_experts_f4: x")
-    _f4_tensor(y, (torch.float32,), "tq_linear_experts_f4: y")
+    dev = _f4_device(ids, "tq_linear_experts_f4: ids")
+    _f4_tensor(ids, (torch.int32,), dev, "tq_linear_experts_f4: ids")
+    _f4_tensor(x, _BF16, dev, "tq_linear_experts_f4: x")
+    _f4_tensor(y, _F32, dev, "tq_linear_experts_f4: y")
     if ids.dim() != 1 or x.dim() != 2 or y.dim() != 2:
         raise TqError(TQ_ERR_SHAPE, "tq_linear_experts_f4: ids, x, y")
     if w.desc.format in F4_BLOCK:
