@@ -704,11 +704,12 @@ cudaError_t dispatch(const WeightsView &w, const WeightsView &x, const Args &a,
                      cudaStream_t stream) {
   if (x.n <= 32) return launch<FMT, 32, 1>(w, x, a, stream);
   if (x.n <= 64) return launch<FMT, 64, 1>(w, x, a, stream);
-  // A wave of 256 x 256 tiles takes 7/5 of the time of a wave of 128 x 128
-  // tiles, two of which cover half of it (measured per 32 stages on 148 SMs:
-  // 14.1 and 10.1 us), so the large tile wins where its waves are full: 98
-  // against 129 us at 21504 x 5376 x 2048 rows, but 38 against 29 us at
-  // 5376 x 8192 x 777 rows (84 tiles on 74 pairs).
+  // A wave of 256 x 256 tiles takes about 7/5 of the time of a wave of 128 x
+  // 128 tiles, two of which cover half of it, so the large tile wins where its
+  // waves are full: MX4 (NV4) 101 (113) against 129 (150) us at 21504 x 5376 x
+  // 2048 rows, but 30 (36) against 22 (25) us at 5376 x 8192 x 777 rows (84
+  // tiles on 74 pairs) and 9.8 (9.2) against 5.8 (6.1) us at 1024 x 1024 x
+  // 1024.
   int dev = 0, sms = 148;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
