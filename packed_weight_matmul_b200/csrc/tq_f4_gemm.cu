@@ -55,6 +55,7 @@ constexpr int kRowsM = 128;         // weight rows per CTA
 constexpr uint32_t kStageRow = kF4StageRow;
 constexpr uint32_t kTmemColumns = 512;
 constexpr uint32_t kSmemLimit = 227u * 1024u;
+constexpr uint32_t kReserve = 3u * 1024u;  // barriers, alignment, static
 constexpr int kScaleGroups = 2, kDrainWarps = 8;
 constexpr int kScaleWarps = 4;  // of a group, single CTA
 
@@ -81,14 +82,14 @@ struct Plan {
   static constexpr uint32_t kPiece = FMT == TQ_FMT_NV4 ? 16u : 8u;
   static constexpr uint32_t kUnit =
       kCopied ? 32u
-              : kPiece * (5 * kStage + 2 * (kRowsM + NT) * 4 * kPiece + 3072u <=
+              : kPiece * (5 * kStage + 2 * (kRowsM + NT) * 4 * kPiece + kReserve <=
                                   kSmemLimit
                               ? 4u
                               : 2u);
   static constexpr uint32_t kScales = kCopied ? 0 : (kRowsM + NT) * kUnit;
   static constexpr int kUnitStages = (int)(kUnit / kScaleRow);
   static constexpr int kFit =
-      (int)((kSmemLimit - 3072u - kScaleGroups * kScales) / kStage);
+      (int)((kSmemLimit - kReserve - kScaleGroups * kScales) / kStage);
   static constexpr int kFitT = (int)((kTmemColumns - NT) / kScaleCols);
   static constexpr int kStages0 = kFit < kFitT ? kFit : kFitT;
   static constexpr int kStages = kStages0 < 8 ? kStages0 : 8;
