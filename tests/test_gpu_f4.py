@@ -643,6 +643,28 @@ def test_experts_binding_refusals():
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("n,k,b", [(130, 288, 1), (130, 288, 7), (257, 544, 30),
+                                   (300, 288, 70), (2080, 4128, 40),
+                                   (640, 512, 300)])
+def test_rows_behind_the_batch(fmt, n, k, b):
+    """y may have more rows than the batch; they stay as they were."""
+    tq = U.tq()
+    codes, scales = exact_package(fmt, n, k, 4)
+    w = weights(fmt, F.pack(codes), scales, None)
+    cx, sx = exact_package(fmt, b, k, 5)
+    xw = weights(fmt, F.pack(cx), sx, None)
+    x = integers(b, k, 6)
+    ids = torch.zeros(b, dtype=torch.int32, device=U.DEV)
+    for run in (lambda y: tq.tq_linear(w, x, y),
+                lambda y: tq.tq_linear_f4(w, xw, y),
+                lambda y: tq.tq_linear_experts_f4(w, 1, ids, x, y)):
+        y = torch.full((b + 40, n), 7.0, device=U.DEV)
+        run(y)
+        torch.cuda.synchronize()
+        assert (y[b:] == 7.0).all()
+
+
 # ---- in a row -----------------------------------------------------------------------
 
 @pytest.mark.parametrize("fmt", FMTS)
