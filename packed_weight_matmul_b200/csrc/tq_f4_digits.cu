@@ -109,21 +109,28 @@ __global__ void __launch_bounds__(256)
 
 // 0 where the plain kernels do as well. Measured (us; plain, digits):
 //   MX4  21504 x 5376 batch 4: 23, 16.5; 16: 43, 23; 64: 113, 40
-//        5376 x 21504 batch 4: 28, 20; 8192 x 5376 batch 4: 13.5, 11
-//        4096 x 4096 batch 8: 6.7, 11; 32: 12.7, 11.7; 48: 17.8, 11.9
+//        5376 x 21504 batch 4: 28, 20.6; 16: 33, 32; 32: 50, 35.5
+//        8192 x 5376 batch 4: 13.5, 11; 4096 x 4096 batch 8: 7.4, 9.4; 32:
+//        12.8, 11.6; 48: 17.8, 11.9; 2048 x 8192 batch 16: 10, 15; 32: 12.6,
+//        15.4
 //   NV4  21504 x 5376 batch 4: 29, 20; 16: 42, 28; 64: 107, 56
-//        5376 x 21504 batch 4: 22.6, 24; 16: 31, 37; 64: 76, 66
-//        4096 x 4096 batch 32: 12.4, 12.2; 48: 17.3, 12.5
+//        8192 x 5376 batch 4: 12.0, 12.8; 16: 15.8, 15.1; 32: 23.5, 18
+//        5376 x 21504 batch 4: 22.7, 23.5; 16: 32, 37.5; 32: 48, 40
+//        2048 x 21504 batch 16: 19, 37; 32: 25, 36
 //        1000 x 4000 batch 64: 9.3, 14.5; 130: 19.6, 15.9
 //        128 x 512 batch 64: 4.2, 6.6; 300: 4.5, 7.2
 // The second launch costs 4 us, and long rows of x cost more digits for the
-// same weights, which the larger part of NV4 shows. The plain kernel slows down
-// past 32 rows unless it has room for passes of 8 or 16 next to one another.
+// same weights. The plain kernel slows down past 16 and again past 32 rows
+// unless it has room for passes of 8 or 16 next to one another; the product
+// of the digits, which does not split K, needs many weight rows to fill the
+// GPU.
 int64_t digits_f4_workspace(const WeightsView &w, int64_t batch) {
   const int64_t weights = w.n * w.k;
-  const bool large = batch >= 3 && weights >= (1 << 25) &&
-                     (w.format == TQ_FMT_MX4 || w.n >= w.k);
-  const bool wide = batch > 32 && rows_per_pass_f4(w, 1, batch) > 16;
+  const bool large = batch >= 3 && (w.format == TQ_FMT_MX4
+                                        ? weights >= (1 << 25)
+                                        : weights >= (1 << 26) && w.n >= w.k);
+  const bool wide = batch > (w.n >= 4096 ? 16 : 32) &&
+                    rows_per_pass_f4(w, 1, batch) > 16;
   if (!(large || wide) || !decode_f4_supported(w, 1)) return 0;
   return layout_of(w.format, batch, w.k).total;
 }

@@ -420,10 +420,11 @@ def linear_ws(w, x, used=True):
 
 
 # n, k, batches: many weights from 3 rows on (NV4: n >= k), fewer weights past
-# 32 rows; ragged tiles, a last stage of 32 to 160 codes, several chunks of
+# 16 or 32 rows; ragged tiles, a last stage of 32 to 160 codes, several chunks of
 # 512 rows
 DIGITS = [(MX4, 4096, 8192, (3, 5, 8, 9, 20)), (MX4, 1003, 33472, (4, 7)),
-          (NV4, 8200, 4128, (3, 8, 13, 33)), (NV4, 5800, 5792, (5, 17)),
+          (NV4, 16400, 4128, (3, 8, 13, 33)), (NV4, 5800, 5792, (17, 30)),
+          (MX4, 4100, 4128, (17,)),
           (MX4, 2080, 4128, (33, 65, 130)), (NV4, 2080, 4128, (40, 64, 97)),
           (MX4, 70, 32, (9500,)),
           (MX4, 1100, 1952, (600, 1030)), (NV4, 1100, 1952, (513,))]
@@ -459,7 +460,7 @@ def test_digit_rows_exact(fmt, n, k, batches):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
-@pytest.mark.parametrize("n,k,b", [(8192, 4096, 6), (2080, 4128, 40),
+@pytest.mark.parametrize("n,k,b", [(16384, 4128, 6), (2080, 4128, 40),
                                    (1100, 1952, 515)])
 def test_digit_rows_range(fmt, n, k, b):
     """x over many powers of two inside a row, rows at both ends of the
