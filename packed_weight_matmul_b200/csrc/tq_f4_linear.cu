@@ -13,10 +13,13 @@
 // multiplied by their block's scale in fp16 (exact, see below) and go as the
 // A operand into fp16 mma with fp32 sums; x is the B operand:
 //   NV4  c s has at most 6 significant bits between 2^-10 and 2688: exact.
-//   MX4  the scale is 2^(E - R + 13) with R the largest exponent that this
-//        part of the row has met: c 2^(E - R + 13) is exact down to
-//        2^(R - 27), smaller blocks (below 2^-27 of the row's largest) count
-//        as 0. When R rises the sums are scaled down, exactly.
+//   MX4  the scale is 2^(E - R + 5), exact for R - 19 <= E <= R + 8, with R an
+//        exponent that this part of the row has met. A block above that moves
+//        R to its own exponent, and the sums are scaled down; a stage with a
+//        block below it multiplies its codes block by block, as they are, and
+//        applies 2^(E - R + 5) to the fp32 sums. Blocks of zero codes may carry
+//        any scale and do neither. Blocks below 2^-131 of the row's largest
+//        count as if they lay there.
 //   x    bf16 has 8 significant bits, fp16 11 but a short range: x is held
 //        as x 2^(14 - X) with X the exponent of the largest value of its row
 //        so far, exact down to 2^(X - 31), off by at most 2^(X - 39) below.
@@ -45,6 +48,7 @@ constexpr int kStageK = 256;    // codes of a row per stage
 constexpr int kSegment = 1024;  // ids looked through at once
 constexpr int kList = 2 * kSegment;  // rows of an expert gathered for its passes
 constexpr int kPrefetch = 1024; // bytes of a row hinted to the L2 cache
+constexpr int kTopR = 246;  // R at most: NaN (255) lies outside of its range
 constexpr int kPlaces = 2 * 148;  // CTAs that run at once
 
 struct RowArgs {
@@ -409,51 +413,105 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
               e[r] = odd_byte(r, t) | odd_byte(r, t + 4) << 16;
             }
           }
-          // largest of each row over the quad, row g low, row g + 8 high
-          auto quad_max = [&](uint32_t e0, uint32_t e1) {
-            uint32_t m = __vmaxu2(__byte_perm(e0, e1, 0x5410),
-                                  __byte_perm(e0, e1, 0x7632));
-            m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-            return __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-          };
-          uint32_t now = __vmaxu2(R, quad_max(e[0], e[1]));
-          bool nan = false;
-          if (__any_sync(0xFFFFFFFFu, now != R)) {
-            nan = __any_sync(0xFFFFFFFFu, (now & 0xFFFFu) == 255u ||
-                                              now >> 16 == 255u);
-            if (nan) {  // NaN scales do not count
-              auto drop = [](uint32_t v) {
-                return ((v & 0xFFFFu) == 255u ? 0u : v & 0xFFFFu) |
-                       (v >> 16 == 255u ? 0u : v & 0xFFFF0000u);
-              };
-              now = __vmaxu2(R, quad_max(drop(e[0]), drop(e[1])));
-            }
-            const float f0 =
-                pow2_down((int)(R & 0xFFFFu) - (int)(now & 0xFFFFu));
-            const float f1 = pow2_down((int)(R >> 16) - (int)(now >> 16));
+          if (st == 0) {  // a guess: the largest exponent in the stage
+            R = __vmaxu2(__byte_perm(e[0], e[1], 0x5410),
+                         __byte_perm(e[0], e[1], 0x7632));
+            R = __vmaxu2(R, __shfl_xor_sync(0xFFFFFFFFu, R, 1));
+            R = __vmaxu2(R, __shfl_xor_sync(0xFFFFFFFFu, R, 2));
+            R = __vminu2(R, kTopR * 0x00010001u);
+          }
+          // blocks outside of what fp16 holds beside R
+          bool odd = false;
 #pragma unroll
-            for (int c = 0; c < kTiles; ++c) {
-              acc[c][0] *= f0;
-              acc[c][1] *= f0;
-              acc[c][2] *= f1;
-              acc[c][3] *= f1;
+          for (int r = 0; r < 2; ++r) {
+            const uint32_t top = __byte_perm(R, 0, r == 0 ? 0x1010 : 0x3232);
+            odd |= __vmaxu2(e[r], top + 0x00080008u) != top + 0x00080008u ||
+                   __vminu2(e[r] + 0x00130013u, top) != top;
+          }
+          if (__any_sync(0xFFFFFFFFu, odd)) {
+            bool small = false;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              // exponents of the blocks with any weight, else -1; NaN apart
+              const int was = (int)(R >> (16 * r) & 0xFFFFu);
+              int E[2], now = -1;
+              bool nan = false;
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint4 c = lds128(src + 8 * r * (kStageK / 2) +
+                                       (h == 0 ? my_chunk : my_chunk ^ 64u));
+                const int b = (int)(e[r] >> (16 * h) & 0xFFu);
+                nan |= b == 255;
+                E[h] = b != 255 && ((c.x | c.y | c.z | c.w) & 0x77777777u) != 0
+                           ? b
+                           : -1;
+                now = max(now, E[h]);
+              }
+              now = max(now, __shfl_xor_sync(0xFFFFFFFFu, now, 1));
+              now = max(now, __shfl_xor_sync(0xFFFFFFFFu, now, 2));
+              // (with no sums yet R may fall as well)
+              now = st > 0 && now <= was + 8 ? was : min(max(now, 0), kTopR);
+              const uint32_t nans = __ballot_sync(0xFFFFFFFFu, nan);
+              // a NaN scale makes the row NaN, whatever the codes
+              const bool gone = (nans >> (lane & 28) & 15u) != 0;
+              const float f = pow2_down(min(was - now, 0));
+#pragma unroll
+              for (int c = 0; c < kTiles; ++c) {
+                acc[c][2 * r] =
+                    gone ? __int_as_float(0x7FC00000) : acc[c][2 * r] * f;
+                acc[c][2 * r + 1] =
+                    gone ? __int_as_float(0x7FC00000) : acc[c][2 * r + 1] * f;
+              }
+              R += (uint32_t)(now - was) << (16 * r);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                if (E[h] < 0) E[h] = now;  // weighs nothing
+                small |= E[h] + 19 < now;
+              }
+              e[r] = (uint32_t)E[0] | (uint32_t)E[1] << 16;
             }
-            R = now;
+            if (__any_sync(0xFFFFFFFFu, small)) {
+              // Word i % 4 of block i / 4: the lanes that hold another block
+              // feed zeros on both sides (0 times Inf would be NaN).
+#pragma unroll 1
+              for (int i = 0; i < 32; ++i) {
+                const uint32_t here = t == (i >> 2 & 3) ? 0xFFFFFFFFu : 0u;
+                const uint32_t at =
+                    src + (my_chunk ^ (i >> 4 << 6)) + 4 * (i & 3);
+                const uint32_t xs = xat + 256 * (i >> 4) + 64 * (i & 3);
+                uint32_t p[4], q[4];
+                f4x8_to_h2(lds32(at) & here, p);
+                f4x8_to_h2(lds32(at + 8 * (kStageK / 2)) & here, q);
+                float f[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                  const uint32_t both =
+                      __shfl_sync(0xFFFFFFFFu, e[r], i >> 2 & 3, 4);
+                  const int E = (int)(both >> (16 * (i >> 4)) & 0xFFu);
+                  const int field = E - (int)(R >> (16 * r) & 0xFFFFu) + 132;
+                  f[r] = __int_as_float(max(field, 1) << 23);
+                }
+#pragma unroll
+                for (int c = 0; c < kTiles; ++c) {
+                  const uint4 v = lds128(xs + 8 * c * P::kXPitch);
+                  float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                  mma_f16(d, p[0], q[0], p[1], q[1], v.x & here, v.y & here);
+                  mma_f16(d, p[2], q[2], p[3], q[3], v.z & here, v.w & here);
+#pragma unroll
+                  for (int k = 0; k < 4; ++k)
+                    acc[c][k] = fmaf(d[k], f[k >> 1], acc[c][k]);
+                }
+              }
+              continue;
+            }
           }
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            // exponent fields E - R + 28 of both chunks, at least 0: kept
-            // 256 too large while they may be negative
-            const uint32_t d = (r == 0 ? R & 0xFFFFu : R >> 16) * 0x00010001u;
-            const uint32_t v =
-                __vmaxu2(e[r] + 0x011C011Cu - d, 0x01000100u) & 0x00FF00FFu;
+            // exponent fields E - R + 20 of both chunks, 1 to 28
+            const uint32_t v = e[r] + 0x00140014u -
+                               __byte_perm(R, 0, r == 0 ? 0x1010 : 0x3232);
             f[0][r][0] = f[0][r][1] = __byte_perm(v, 0, 0x1010) << 10;
             f[1][r][0] = f[1][r][1] = __byte_perm(v, 0, 0x3232) << 10;
-            if (nan) {
-              if ((e[r] & 0xFFFFu) == 255u)
-                f[0][r][0] = f[0][r][1] = 0x7E007E00u;
-              if (e[r] >> 16 == 255u) f[1][r][0] = f[1][r][1] = 0x7E007E00u;
-            }
           }
         } else {
 #pragma unroll
@@ -548,7 +606,7 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
       for (int j = 0; j < 4; ++j) {
         const int b = 8 * i + 2 * t + (j & 1);
         int e = s_exp[b] - 14;
-        if (FMT == TQ_FMT_MX4) e += (int)(j < 2 ? R & 0xFFFFu : R >> 16) - 140;
+        if (FMT == TQ_FMT_MX4) e += (int)(j < 2 ? R & 0xFFFFu : R >> 16) - 132;
         part[b * P::kPartPitch + 16 * warp + g + (j < 2 ? 0 : 8)] =
             scalbnf(acc[i][j], e);
       }

@@ -49,6 +49,12 @@ __device__ __forceinline__ uint4 lds128(uint32_t at) {
   return v;
 }
 
+__device__ __forceinline__ uint32_t lds32(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+
 __device__ __forceinline__ uint32_t lds_u8(uint32_t at) {
   uint32_t v;
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at) : "memory");

@@ -1,0 +1,130 @@
+"""GPU tests of the 4-bit products where the values, not the sizes, are the
+hard part: block scales far apart, all-zero blocks under large scales, Inf
+against small blocks, intermediate results outside fp32's range, every digit of
+the digit rows, long sums of one sign. References in 64 bits (f4_util)."""
+import pytest
+import torch
+
+from tests import f4_util as F
+from tests import gpu_util as U
+from tests.test_gpu_f4 import (MX4, exact_package, gen, integers, run_linear,
+                               weights)
+
+pytestmark = pytest.mark.gpu
+
+# one of each kernel and row count per pass: digits made on the spot, the row
+# kernel with 8, 16, 32 and 64 rows
+BATCHES = [1, 3, 5, 12, 20, 64]
+
+
+def plain_linear(w, x):
+    """tq_linear of the C ABI: never a workspace."""
+    tq, b = U.tq(), x.shape[0]
+    y = torch.full((b, w.n), float("nan"), device=U.DEV)
+    assert tq.lib().tq_linear(w.desc, x.data_ptr(), b, x.stride(0),
+                              y.data_ptr(), w.n, None) == tq.TQ_OK
+    torch.cuda.synchronize()
+    return y
+
+
+def run_experts(w, E, ids, x):
+    y = torch.full((x.shape[0], w.n), float("nan"), device=U.DEV)
+    U.tq().tq_linear_experts_f4(w, E, ids, x, y)
+    torch.cuda.synchronize()
+    return y
+
+
+def expert_ids(t, E, seed=5):
+    return torch.randint(0, E, (t,), generator=gen(seed), device=U.DEV,
+                         dtype=torch.int32)
+
+
+def expert_ref(w64, ids, x, n):
+    w64 = w64.view(-1, n, w64.shape[1])
+    return torch.stack([w64[e] @ r for e, r in zip(ids.tolist(), x.double())])
+
+
+def same(y, ref, what):
+    """Equal, NaN and Inf in the same places."""
+    nan = torch.isnan(ref)
+    assert torch.equal(torch.isnan(y), nan), f"{what}: NaN"
+    assert torch.equal(y.double()[~nan], ref[~nan]), what
+
+
+def every_path(fmt, codes, scales, g, x_of, n, what):
+    """x_of(rows): bf16 rows whose products with the package are exact in fp32.
+    Compares every kernel for bf16 rows; g: tensor scale (float) or None."""
+    w64 = F.values(codes, scales, fmt) * (1.0 if g is None else g)
+    gt = None if g is None else torch.full((1,), g, device=U.DEV)
+    w = weights(fmt, F.pack(codes), scales, gt)
+    for b in BATCHES:
+        x = x_of(b)
+        ref = x.double() @ w64.t()
+        same(run_linear(w, x), ref, f"{what}, {b} rows")
+        same(plain_linear(w, x), ref, f"{what}, {b} rows, no workspace")
+    E = codes.shape[0] // n
+    ge = None if g is None else gt.repeat(E)
+    we = weights(fmt, F.pack(codes), scales, ge, n, codes.shape[1])
+    for t in (E, 5 * E + 1, 40 * E):
+        x, ids = x_of(t), expert_ids(t, E)
+        same(run_experts(we, E, ids, x), expert_ref(w64, ids, x, n),
+             f"{what}, {t} rows over {E} experts")
+
+
+KS = [1056, 1024]  # a ragged last stage; rows of whole stages
+
+
+# ---- MX4 block scales ------------------------------------------------------------
+
+@pytest.mark.parametrize("k", KS)
+@pytest.mark.parametrize("low,zero", [(126, 200), (126, 254), (20, 254),
+                                      (1, 160)])
+def test_zero_block_under_large_scale(k, low, zero):
+    """A block of zero codes may carry any scale: it weighs nothing, and the
+    other blocks keep their values."""
+    n, E = 70, 4
+    codes, scales = exact_package(MX4, n * E, k, 1)
+    scales = (scales.int() + low - 126).to(torch.uint8)
+    for j in (0, 3, k // 32 - 1):
+        codes[:, 32 * j:32 * j + 32] &= 8
+        scales[:, j] = zero
+    scales[5] = zero  # a row of zeros under large scales
+    codes[5] = 0
+    s = 2.0 ** (100 if low < 126 else 0)
+    every_path(MX4, codes, scales, None,
+               lambda b: (integers(b, k, b) * s).bfloat16(), n, "zero blocks")
+
+
+@pytest.mark.parametrize("k", KS)
+@pytest.mark.parametrize("down", [28, 60, 110])
+def test_small_blocks_count(k, down):
+    """Blocks far below the row's largest keep their values: x is 0 where the
+    large blocks are."""
+    n, E = 70, 4
+    codes, scales = exact_package(MX4, n * E, k, 3)
+    small = torch.arange(k // 32, device=U.DEV) % 3 == 1
+    scales[:, small] -= down
+    mask = small.repeat_interleave(32)
+
+    def x_of(b):
+        return torch.where(mask, integers(b, k, b), 0).bfloat16()
+    every_path(MX4, codes, scales, None, x_of, n, "small blocks")
+
+
+@pytest.mark.parametrize("k", KS)
+def test_inf_against_small_blocks(k):
+    """Inf times a small weight is Inf, not NaN."""
+    n, E = 70, 4
+    codes, scales = exact_package(MX4, n * E, k, 4)
+    scales[:, 2] = 90
+    scales[:, 5] = 4
+    codes[:, 64:96] |= 1  # no 0 * Inf
+    codes[:, 160:192] |= 1
+
+    def x_of(b):
+        x = integers(b, k, b)
+        x[:, 64:96], x[:, 160:192] = 0, 0
+        x[0, 70] = float("inf")
+        x[b // 2, 165] = -float("inf")
+        return x
+    every_path(MX4, codes, scales, None, x_of, n, "Inf")
