@@ -7,13 +7,16 @@
 //   after 8 digits the rest is at most 2^-23 of the block's largest value.
 //   All of -4 .. 4 are E2M1 values. Row 8 b + i of the B operand holds d_i of
 //   row b of x.
-//   MX4: its block scale 2^(f - X - 1 - 3 i) is an E8M0 byte, X the exponent
-//        of the largest value of the row in this CTA's slice of K.
+//   MX4: its block scale 2^(f - T - 1 - 3 i) is an E8M0 byte. T = 0, so that
+//        the sums leave fp32's range only where y does, except for rows (slices
+//        of K) whose largest value has an exponent X below -40: T = X + 40.
+//        Digits whose scale falls below 2^-127 take that one: off by 2^-80 of
+//        the row's largest at most.
 //   NV4: an E4M3 byte reaches from 2^-9 to 2^8 only, so row i has a factor
 //        2^(X - 9 - 3 i) of its own, applied to its sum, and the block scale
 //        2^(f - X + 8); blocks below 2^-17 of the row's largest take the
 //        smallest scale, which leaves them off by 2^-40 of it.
-//   y = 2^X sum_i D_i (MX4) or 2^(X - 9) sum_i 8^-i D_i (NV4), D the fp32
+//   y = 2^T sum_i D_i (MX4) or 2^(X - 9) sum_i 8^-i D_i (NV4), D the fp32
 //   accumulators. NaN and Inf count as 0 in the digits; their rows of x are
 //   flagged and the products with them added to the sums afterwards.
 #pragma once
@@ -79,6 +82,9 @@ __device__ __forceinline__ uint32_t codes8(const F2 (&q)[4]) {
   return r;
 }
 
+// 2^T of a row of exponent X (both biased).
+__device__ __forceinline__ int mx4_reference(int X) { return min(X + 40, 127); }
+
 // Block scale of exponent f (biased, at least 1) in a row of exponent X: the
 // byte of digit 0 (the others of MX4 lie 3, 6, .. below, not under 0) and the
 // exponent field of the factor that brings the block to (-4, 4).
@@ -86,9 +92,8 @@ template <int FMT>
 __device__ __forceinline__ void digit_scale(int f, int X, uint32_t *byte,
                                             uint32_t *field) {
   if (FMT == TQ_FMT_MX4) {
-    const int b = max(126 + f - X, 0);
-    *byte = (uint32_t)b;
-    *field = (uint32_t)(381 - X - b);
+    *byte = (uint32_t)(126 + f - mx4_reference(X));
+    *field = (uint32_t)(255 - f);
   } else {
     const int e = max(f - X + 8, -9);
     *byte = e >= -6 ? (uint32_t)(e + 7) << 3 : 1u << (e + 9);
@@ -132,6 +137,7 @@ __device__ __forceinline__ float digit_sum(const uint32_t *d, int X) {
   for (int i = 6; i >= 0; --i)
     t = FMT == TQ_FMT_MX4 ? t + __uint_as_float(d[i])
                           : fmaf(t, 0.125f, __uint_as_float(d[i]));
+  if (FMT == TQ_FMT_MX4) X = mx4_reference(X);
   if (FMT == TQ_FMT_NV4) t *= 0.001953125f;  // 2^-9
   return t * __uint_as_float((uint32_t)X << 23);
 }

@@ -7,8 +7,8 @@ import torch
 
 from tests import f4_util as F
 from tests import gpu_util as U
-from tests.test_gpu_f4 import (MX4, exact_package, gen, integers, run_linear,
-                               weights)
+from tests.test_gpu_f4 import (MX4, exact_package, gen, integers, linear_ws,
+                               run_linear, weights)
 
 pytestmark = pytest.mark.gpu
 
@@ -128,3 +128,45 @@ def test_inf_against_small_blocks(k):
         x[b // 2, 165] = -float("inf")
         return x
     every_path(MX4, codes, scales, None, x_of, n, "Inf")
+
+
+@pytest.mark.parametrize("k", KS)
+def test_nan_scale_beside_the_largest(k):
+    """A NaN scale next to scales of 250 to 254, from the first block on or
+    later; zero codes under it."""
+    n, E = 70, 4
+    codes, scales = exact_package(MX4, n * E, k, 5)
+    scales = (scales.int() + 124).to(torch.uint8).clamp_max(254)
+    for r, j in ((3, 0), (9, 7), (69, k // 32 - 1), (140, 1)):
+        scales[r, j] = 255
+    codes[9, 7 * 32:8 * 32] = 0
+    every_path(MX4, codes, scales, None,
+               lambda b: (integers(b, k, b) * 2.0 ** -60).bfloat16(), n, "NaN")
+
+
+# ---- range -----------------------------------------------------------------------
+
+@pytest.mark.parametrize("k", KS)
+@pytest.mark.parametrize("shift,e", [(122, -80), (-118, 100), (90, 20),
+                                     (0, -120), (60, -120)])
+def test_scales_and_x_at_opposite_ends(k, shift, e):
+    """Large weights times small x, and the other way round."""
+    n, E = 70, 4
+    codes, scales = exact_package(MX4, n * E, k, 6)
+    scales = (scales.int() + shift).to(torch.uint8)
+    every_path(MX4, codes, scales, None,
+               lambda b: (integers(b, k, b).double() * 2.0 ** e).bfloat16(), n,
+               "opposite ends")
+
+
+@pytest.mark.parametrize("fmt,n,k,b", [(MX4, 4096, 8192, 5),
+                                       (MX4, 2080, 4128, 40)])
+def test_digit_rows_at_opposite_ends(fmt, n, k, b):
+    codes, scales = exact_package(fmt, n, k, 8)
+    codes &= 11  # partial sums below 2^22 in steps of 1/4
+    for shift, e in ((122, -80), (-118, 100)):
+        x = (integers(b, k, b).double() * 2.0 ** e).bfloat16()
+        s = (scales.int() + shift).to(torch.uint8)
+        w = weights(fmt, F.pack(codes), s)
+        same(linear_ws(w, x), x.double() @ F.values(codes, s, fmt).t(),
+             f"2^{shift}")
