@@ -44,6 +44,28 @@ __device__ __forceinline__ float f4_scale(uint32_t b) {
   return FMT == TQ_FMT_MX4 ? e8m0_to_f32(b) : e4m3_to_f32(b);
 }
 
+// A tensor scale g = m 2^e with |m| < 1 (0, NaN and Inf as they are): sums may
+// lie outside of fp32's range where g brings them back, so m is applied first
+// and e together with the other exponents.
+struct TensorScale {
+  float m;
+  int e;
+};
+
+__device__ __forceinline__ TensorScale tensor_scale(float g) {
+  TensorScale s = {g, 0};
+  if (fabsf(g) < __int_as_float(0x7F800000)) s.m = frexpf(g, &s.e);
+  return s;
+}
+
+// v 2^e in two steps, for |e| up to 284: below 2^-252 the power is that, which
+// leaves 0 of a sum all the same.
+__device__ __forceinline__ float times_pow2(float v, int e) {
+  const int half = max(e >> 1, -126), rest = max(e - half, -126);
+  return v * __int_as_float((half + 127) << 23) *
+         __int_as_float((rest + 127) << 23);
+}
+
 // All threads of a cluster meet. Relaxed: it orders no memory (the ordinary
 // barrier waits until this CTA's global stores are acknowledged, about 1 us),
 // which is enough where CTAs only tell one another that they have finished

@@ -467,12 +467,15 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
       if (warp < 10) {
+        const float wg = a.wg != nullptr ? a.wg[expert] : 1.0f;
         const bool ok0 = mbar_wait(dfull, (uint32_t)pass_no & 1u, abort_addr,
                                    kWaitLimitNs);
         const bool ok = __all_sync(0xFFFFFFFFu, ok0);
         tc_fence_after_sync();
         const int q = warp & 3, r = 32 * q + lane;
         float *part = reinterpret_cast<float *>(smem_raw + (base - smem_u32(smem_raw)));
+        const TensorScale ts = FMT == TQ_FMT_NV4 ? tensor_scale(wg)
+                                                 : TensorScale{1.0f, 0};
 #pragma unroll 1
         for (int c = 0; c < rows * P::kTerms; c += 16) {
           uint32_t v[16];
@@ -485,9 +488,9 @@ __global__ void __launch_bounds__(kThreads, 2)
               const int b = c / 8 + h;
               if (8 * b >= rows) break;
               const int64_t at = b0 / 8 + b;
-              float t = digit_sum<FMT>(&v[8 * h], D.exps[at]);
+              float t = digit_sum<FMT>(&v[8 * h], D.exps[at], ts);
               if (D.odd[at] && row0 + r < a.n)
-                t += odd_products<FMT>(D.x + at * D.ldx, (int)k0, (int)k1,
+                t += wg * odd_products<FMT>(D.x + at * D.ldx, (int)k0, (int)k1,
                                        a.codes, a.wscales, wrow + r, a.k);
               part[b * P::kPitch + r] = ok ? t : __int_as_float(0x7FC00000);
             }
@@ -502,9 +505,9 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int h = 0; h < 2; ++h) {
               const int b = c / 8 + h;
               if (b >= rows) break;
-              float t = digit_sum<FMT>(&v[8 * h], s_exp[b]);
+              float t = digit_sum<FMT>(&v[8 * h], s_exp[b], ts);
               if (s_odd[b] && row0 + r < a.n)
-                t += odd_products<FMT>(x_row(b), (int)k0, (int)k1, a.codes,
+                t += wg * odd_products<FMT>(x_row(b), (int)k0, (int)k1, a.codes,
                                        a.wscales, wrow + r, a.k);
               part[b * P::kPitch + r] = ok ? t : __int_as_float(0x7FC00000);
             }
@@ -518,8 +521,12 @@ __global__ void __launch_bounds__(kThreads, 2)
       cooperative_groups::this_cluster().sync();
     else
       __syncthreads();
-    float g = a.wg != nullptr ? a.wg[expert] : 1.0f;
-    if (SRC == kPacked && a.xg != nullptr) g *= *a.xg;
+    // (digit_sum has applied the tensor scale)
+    float g = 1.0f;
+    if (SRC == kPacked && per == 1) {
+      if (a.wg != nullptr) g = *a.wg;
+      if (a.xg != nullptr) g *= *a.xg;
+    }
     for (int i = tid + rank * kThreads; i < rows / per * kTile;
          i += ks * kThreads) {
       const int b = i / kTile, r = i % kTile;

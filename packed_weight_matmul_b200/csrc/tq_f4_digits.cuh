@@ -128,18 +128,19 @@ __device__ __forceinline__ void digits8(const uint4 &w, uint32_t field,
   }
 }
 
-// The sum behind a row's 8 accumulators (fp32 bits), without g; the smallest
+// The sum behind a row's 8 accumulators (fp32 bits), times g; the smallest
 // digits are added first.
 template <int FMT>
-__device__ __forceinline__ float digit_sum(const uint32_t *d, int X) {
+__device__ __forceinline__ float digit_sum(const uint32_t *d, int X,
+                                           const TensorScale &g) {
   float t = __uint_as_float(d[7]);
 #pragma unroll
   for (int i = 6; i >= 0; --i)
     t = FMT == TQ_FMT_MX4 ? t + __uint_as_float(d[i])
                           : fmaf(t, 0.125f, __uint_as_float(d[i]));
-  if (FMT == TQ_FMT_MX4) X = mx4_reference(X);
-  if (FMT == TQ_FMT_NV4) t *= 0.001953125f;  // 2^-9
-  return t * __uint_as_float((uint32_t)X << 23);
+  if (FMT == TQ_FMT_MX4)
+    return t * g.m * __uint_as_float((uint32_t)mx4_reference(X) << 23);
+  return times_pow2(t * g.m, X - 127 - 9 + g.e);
 }
 
 // One weight, for the rows of x that hold NaN or Inf.

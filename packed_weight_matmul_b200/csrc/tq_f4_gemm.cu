@@ -552,6 +552,8 @@ __global__ void __launch_bounds__(Plan<FMT, NT, CG>::kThreads, 1)
       uint32_t h[kCols / 2 < 16 ? 16 : kCols / 2] = {};
       if (args.digits.exps != nullptr) {
         const DigitArgs &D = args.digits;
+        const TensorScale ts = FMT == TQ_FMT_NV4 ? tensor_scale(gn)
+                                                 : TensorScale{gn, 0};
 #pragma unroll
         for (int c = 0; c < kCols; c += 16) {
           if (c >= cols) break;
@@ -563,7 +565,7 @@ __global__ void __launch_bounds__(Plan<FMT, NT, CG>::kThreads, 1)
             const int64_t b = (b0 + c) / 8 + j;
             const int e = c + 8 * j < cols ? __ldg(D.exps + b) : 0;
             h[c / 8 + j] =
-                __float_as_uint(digit_sum<FMT>(&v[8 * j], e) * gn);
+                __float_as_uint(digit_sum<FMT>(&v[8 * j], e, ts));
           }
         }
         drained();

@@ -598,17 +598,19 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
     }
     __syncthreads();  // rings are free, exponents are there
 
-    // partial sums in units of y (without g), [row of x][weight row]
+    // partial sums in units of y, [row of x][weight row]
     float *part = reinterpret_cast<float *>(smem);
+    const TensorScale ts = FMT == TQ_FMT_NV4 ? tensor_scale(gw)
+                                             : TensorScale{1.0f, 0};
 #pragma unroll
     for (int i = 0; i < kTiles; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int b = 8 * i + 2 * t + (j & 1);
-        int e = s_exp[b] - 14;
+        int e = s_exp[b] - 14 + ts.e;
         if (FMT == TQ_FMT_MX4) e += (int)(j < 2 ? R & 0xFFFFu : R >> 16) - 132;
         part[b * P::kPartPitch + 16 * warp + g + (j < 2 ? 0 : 8)] =
-            scalbnf(acc[i][j], e);
+            times_pow2(acc[i][j] * ts.m, e);
       }
     if (ks > 1)
       cooperative_groups::this_cluster().sync();
@@ -637,7 +639,7 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
       }
       if (row0 + r < a.n) {
         const int64_t row = a.ids != nullptr ? s_rows[base + b] : b0 + b;
-        a.y[row * a.ldy + row0 + r] = v * gw;
+        a.y[row * a.ldy + row0 + r] = v;
       }
     }
     // the partial tiles have been read: shared memory may change, or go

@@ -7,8 +7,8 @@ import torch
 
 from tests import f4_util as F
 from tests import gpu_util as U
-from tests.test_gpu_f4 import (MX4, exact_package, gen, integers, linear_ws,
-                               run_linear, weights)
+from tests.test_gpu_f4 import (MX4, NV4, exact_package, gen, integers,
+                               linear_ws, run_linear, weights)
 
 pytestmark = pytest.mark.gpu
 
@@ -159,14 +159,33 @@ def test_scales_and_x_at_opposite_ends(k, shift, e):
                "opposite ends")
 
 
+@pytest.mark.parametrize("k", KS)
+@pytest.mark.parametrize("e,g", [(124, -100), (124, -20), (-125, 100),
+                                 (-60, 126), (0, -140)])
+def test_tensor_scale_range(k, e, g):
+    """Sums that leave fp32's range before the tensor scale brings them back."""
+    n, E = 70, 4
+    codes, scales = exact_package(NV4, n * E, k, 7)
+    every_path(NV4, codes, scales, 2.0 ** g,
+               lambda b: (integers(b, k, b).double() * 2.0 ** e).bfloat16(), n,
+               "tensor scale")
+
+
 @pytest.mark.parametrize("fmt,n,k,b", [(MX4, 4096, 8192, 5),
-                                       (MX4, 2080, 4128, 40)])
+                                       (MX4, 2080, 4128, 40),
+                                       (NV4, 16400, 4128, 5),
+                                       (NV4, 2080, 4128, 40)])
 def test_digit_rows_at_opposite_ends(fmt, n, k, b):
     codes, scales = exact_package(fmt, n, k, 8)
     codes &= 11  # partial sums below 2^22 in steps of 1/4
-    for shift, e in ((122, -80), (-118, 100)):
+    for shift, e in ((122, -80), (-118, 100)) if fmt == MX4 else (
+            (-100, 124), (100, -125)):
         x = (integers(b, k, b).double() * 2.0 ** e).bfloat16()
-        s = (scales.int() + shift).to(torch.uint8)
-        w = weights(fmt, F.pack(codes), s)
-        same(linear_ws(w, x), x.double() @ F.values(codes, s, fmt).t(),
+        if fmt == MX4:
+            s, g, f = (scales.int() + shift).to(torch.uint8), None, 1.0
+        else:
+            s, f = scales, 2.0 ** shift
+            g = torch.full((1,), f, device=U.DEV)
+        w = weights(fmt, F.pack(codes), s, g)
+        same(linear_ws(w, x), x.double() @ (F.values(codes, s, fmt) * f).t(),
              f"2^{shift}")
