@@ -66,6 +66,19 @@ __device__ __forceinline__ float times_pow2(float v, int e) {
          __int_as_float((rest + 127) << 23);
 }
 
+// v g_w g_x = v b a. b is 1 unless g_w g_x lies outside of fp32's range; then
+// each factor has half of its exponent (more than 2^127 changes no result).
+struct Factors {
+  float a, b;
+};
+
+__device__ __forceinline__ Factors scale_factors(float gw, float gx) {
+  const TensorScale w = tensor_scale(gw), x = tensor_scale(gx);
+  const int e = w.e + x.e;
+  if (e >= -124 && e <= 128) return {scalbnf(w.m * x.m, e), 1.0f};
+  return {scalbnf(w.m * x.m, e - e / 2), scalbnf(1.0f, min(e / 2, 127))};
+}
+
 // All threads of a cluster meet. Relaxed: it orders no memory (the ordinary
 // barrier waits until this CTA's global stores are acknowledged, about 1 us),
 // which is enough where CTAs only tell one another that they have finished

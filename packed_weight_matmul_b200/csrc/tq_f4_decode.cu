@@ -120,6 +120,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   __shared__ int s_rows[SRC == kBf16 ? kSegment : 1];
   __shared__ int s_count[kSegment / 32 + 2];
   __shared__ int s_exp[P::kRows], s_odd[P::kRows];
+  __shared__ Factors s_both;  // packed x: both tensor scales
   __shared__ uint32_t s_map[SRC == kBf16 ? kMapExperts / 32 : 1];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -291,6 +292,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     };
 
+    if (FMT == TQ_FMT_NV4 && SRC == kPacked && tid == kThreads - 1)
+      s_both = scale_factors(a.wg != nullptr ? *a.wg : 1.0f,
+                             a.xg != nullptr ? *a.xg : 1.0f);
     if (warp == 0) {
       if (lane == 0) {
         bool ok = true;
@@ -521,12 +525,6 @@ __global__ void __launch_bounds__(kThreads, 2)
       cooperative_groups::this_cluster().sync();
     else
       __syncthreads();
-    // (digit_sum has applied the tensor scale)
-    float g = 1.0f;
-    if (SRC == kPacked && per == 1) {
-      if (a.wg != nullptr) g = *a.wg;
-      if (a.xg != nullptr) g *= *a.xg;
-    }
     for (int i = tid + rank * kThreads; i < rows / per * kTile;
          i += ks * kThreads) {
       const int b = i / kTile, r = i % kTile;
@@ -548,7 +546,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         v += u;
       }
-      v *= g;
+      // (digit_sum has applied the tensor scale)
+      if (FMT == TQ_FMT_NV4 && SRC == kPacked && per == 1)
+        v = v * s_both.b * s_both.a;
       if (row0 + r < a.n) {
         const int64_t row =
             a.ids != nullptr ? s_rows[first + b] : b0 / per + b;

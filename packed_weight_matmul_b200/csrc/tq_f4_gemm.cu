@@ -143,11 +143,10 @@ __device__ __forceinline__ void free_columns(uint32_t taddr, uint32_t cols) {
                  : "memory");
 }
 
-// Two accumulator columns times g as bf16, `lo` in the low half.
-__device__ __forceinline__ uint32_t scaled_pair(uint32_t lo, uint32_t hi,
-                                                float g) {
-  const __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(lo) * g,
-                                                 __uint_as_float(hi) * g);
+// Two fp32 values as bf16, `lo` in the low half.
+__device__ __forceinline__ uint32_t bf16_pair(uint32_t lo, uint32_t hi) {
+  const __nv_bfloat162 p =
+      __floats2bfloat162_rn(__uint_as_float(lo), __uint_as_float(hi));
   return *reinterpret_cast<const uint32_t *>(&p);
 }
 
@@ -517,8 +516,11 @@ __global__ void __launch_bounds__(Plan<FMT, NT, CG>::kThreads, 1)
   } else {
     const int q = warp & 3, half = (warp - P::kDrainWarp) >> 2;  // lanes, columns
     constexpr int kCols = NT / 2;
-    const float g = (args.wg != nullptr ? *args.wg : 1.0f) *
-                    (args.xg != nullptr ? *args.xg : 1.0f);
+    const float g = args.wg != nullptr ? *args.wg : 1.0f;
+    const Factors both =
+        FMT == TQ_FMT_NV4
+            ? scale_factors(g, args.xg != nullptr ? *args.xg : 1.0f)
+            : Factors{1.0f, 1.0f};
     // bf16 pairs need an even row pitch and a 4-byte aligned y
     const bool pairs = args.y_bf16 && args.ldy % 2 == 0 && args.n % 2 == 0 &&
                        (reinterpret_cast<uintptr_t>(args.y) & 3u) == 0;
@@ -533,7 +535,18 @@ __global__ void __launch_bounds__(Plan<FMT, NT, CG>::kThreads, 1)
       const int64_t b0 = (int64_t)(t % args.tiles_n) * NT + half * kCols;
       const int cols = (int)(args.batch - b0 < kCols ? args.batch - b0 : kCols);
       const uint32_t src = kTmem + half * kCols + ((uint32_t)q << 21);
-      const float gn = ok ? g : __int_as_float(0x7FC00000);
+      const float gn = ok ? both.a : __int_as_float(0x7FC00000);
+      // accumulators times the tensor scales, two at once
+      auto scale = [&](uint32_t (&v)[16]) {
+        const F2 a = pack2(gn, gn), b = pack2(both.b, both.b);
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+          F2 p = pack2(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+          if (FMT == TQ_FMT_NV4) p = mul2(p, b);
+          p = mul2(p, a);
+          asm("mov.b64 {%0, %1}, %2;" : "=r"(v[j]), "=r"(v[j + 1]) : "l"(p.v));
+        }
+      };
       auto drained = [&]() {  // the accumulator may be written again
         tc_fence_before_sync();
         __syncwarp();
@@ -552,8 +565,9 @@ __global__ void __launch_bounds__(Plan<FMT, NT, CG>::kThreads, 1)
       uint32_t h[kCols / 2 < 16 ? 16 : kCols / 2] = {};
       if (args.digits.exps != nullptr) {
         const DigitArgs &D = args.digits;
-        const TensorScale ts = FMT == TQ_FMT_NV4 ? tensor_scale(gn)
-                                                 : TensorScale{gn, 0};
+        const float one = ok ? g : __int_as_float(0x7FC00000);
+        const TensorScale ts = FMT == TQ_FMT_NV4 ? tensor_scale(one)
+                                                 : TensorScale{one, 0};
 #pragma unroll
         for (int c = 0; c < kCols; c += 16) {
           if (c >= cols) break;
@@ -593,9 +607,10 @@ __global__ void __launch_bounds__(Plan<FMT, NT, CG>::kThreads, 1)
           uint32_t v[16];
           tmem_ld16(src + c, v);
           tmem_ld_wait();
+          scale(v);
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            h[c / 2 + j] = scaled_pair(v[2 * j], v[2 * j + 1], gn);
+            h[c / 2 + j] = bf16_pair(v[2 * j], v[2 * j + 1]);
         }
         drained();
         __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(args.y);
@@ -635,9 +650,9 @@ __global__ void __launch_bounds__(Plan<FMT, NT, CG>::kThreads, 1)
             uint32_t v[16];
             tmem_ld16(src + c + i, v);
             tmem_ld_wait();
+            scale(v);
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              h[i + j] = __float_as_uint(__uint_as_float(v[j]) * gn);
+            for (int j = 0; j < 16; ++j) h[i + j] = v[j];
           }
           if (c + kHeld >= kCols) drained();
           if (row < args.n) {

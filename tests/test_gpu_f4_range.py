@@ -189,3 +189,27 @@ def test_digit_rows_at_opposite_ends(fmt, n, k, b):
         w = weights(fmt, F.pack(codes), s, g)
         same(linear_ws(w, x), x.double() @ (F.values(codes, s, fmt) * f).t(),
              f"2^{shift}")
+
+
+@pytest.mark.parametrize("n,k,b", [(130, 288, 20), (257, 544, 130),
+                                   (640, 512, 513)])
+@pytest.mark.parametrize("gw,gx,s", [(-75, -75, 0x78), (65, 65, 0x01),
+                                     (100, -120, 0x38), (-140, 126, 0x38)])
+def test_product_tensor_scales(n, k, b, gw, gx, s):
+    """The product of the tensor scales may lie outside fp32's range."""
+    cw, _ = exact_package(NV4, n, k, 9)
+    cx, _ = exact_package(NV4, b, k, 10)
+    cw, cx = cw & 11, cx & 11  # 0, 0.5, 1, 1.5: sums of multiples of 1/4
+    cw[3], cx[b - 1] = 0, 0
+    sw = torch.full((n, k // 16), s, dtype=torch.uint8, device=U.DEV)
+    sx = torch.full((b, k // 16), s, dtype=torch.uint8, device=U.DEV)
+    ts = [torch.full((1,), 2.0 ** e, device=U.DEV) for e in (gw, gx)]
+    ref = F.values(cx, sx, NV4) @ F.values(cw, sw, NV4).t() * \
+        2.0 ** gw * 2.0 ** gx
+    w, x = weights(NV4, F.pack(cw), sw, ts[0]), weights(NV4, F.pack(cx), sx,
+                                                        ts[1])
+    for dtype in (torch.float32, torch.bfloat16):
+        y = torch.full((b, n), float("nan"), device=U.DEV, dtype=dtype)
+        U.tq().tq_linear_f4(w, x, y)
+        torch.cuda.synchronize()
+        assert torch.equal(y, ref.to(dtype))
