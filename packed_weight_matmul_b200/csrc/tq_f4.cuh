@@ -82,7 +82,7 @@ __device__ __forceinline__ Factors scale_factors(float gw, float gx) {
 // All threads of a cluster meet. Relaxed: it orders no memory (the ordinary
 // barrier waits until this CTA's global stores are acknowledged, about 1 us),
 // which is enough where CTAs only tell one another that they have finished
-// reading.
+// reading, and every value read has gone into an instruction issued before.
 __device__ __forceinline__ void cluster_sync_relaxed() {
   asm volatile("barrier.cluster.arrive.relaxed;\n"
                "barrier.cluster.wait;" ::: "memory");

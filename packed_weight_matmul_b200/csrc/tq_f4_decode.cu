@@ -528,6 +528,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int i = tid + rank * kThreads; i < rows / per * kTile;
          i += ks * kThreads) {
       const int b = i / kTile, r = i % kTile;
+      if (row0 + r >= a.n) continue;  // every read is stored, see below
       const uint32_t at = base + (uint32_t)(b * P::kPitch + r) * 4;
       float v = 0.0f;
       for (int c = 0; c < ks; ++c) {
@@ -549,17 +550,16 @@ __global__ void __launch_bounds__(kThreads, 2)
       // (digit_sum has applied the tensor scale)
       if (FMT == TQ_FMT_NV4 && SRC == kPacked && per == 1)
         v = v * s_both.b * s_both.a;
-      if (row0 + r < a.n) {
-        const int64_t row =
-            a.ids != nullptr ? s_rows[first + b] : b0 / per + b;
-        if (a.y_bf16)
-          static_cast<__nv_bfloat16 *>(a.y)[row * a.ldy + row0 + r] =
-              __float2bfloat16_rn(v);
-        else
-          static_cast<float *>(a.y)[row * a.ldy + row0 + r] = v;
-      }
+      const int64_t row = a.ids != nullptr ? s_rows[first + b] : b0 / per + b;
+      if (a.y_bf16)
+        static_cast<__nv_bfloat16 *>(a.y)[row * a.ldy + row0 + r] =
+            __float2bfloat16_rn(v);
+      else
+        static_cast<float *>(a.y)[row * a.ldy + row0 + r] = v;
     }
-    // the partial tiles have been read; what comes next writes there by copies
+    // The partial tiles have been read (each value that was read has gone into
+    // a store, which was issued before this barrier's arrival); what comes next
+    // writes there by copies.
     fence_async();
     if (ks > 1)
       cluster_sync_relaxed();

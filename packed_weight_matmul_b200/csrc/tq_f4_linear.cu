@@ -619,6 +619,7 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
     const uint32_t mine = smem_u32(part);
     for (int i = tid + rank * kThreads; i < rows * kTile; i += ks * kThreads) {
       const int b = i / kTile, r = i % kTile;
+      if (row0 + r >= a.n) continue;  // every read is stored, see below
       const uint32_t at = mine + (b * P::kPartPitch + r) * 4;
       float v = 0.0f;
       if (ks == 1) {
@@ -637,12 +638,12 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
           v += u;
         }
       }
-      if (row0 + r < a.n) {
-        const int64_t row = a.ids != nullptr ? s_rows[base + b] : b0 + b;
-        a.y[row * a.ldy + row0 + r] = v;
-      }
+      const int64_t row = a.ids != nullptr ? s_rows[base + b] : b0 + b;
+      a.y[row * a.ldy + row0 + r] = v;
     }
-    // the partial tiles have been read: shared memory may change, or go
+    // The partial tiles have been read (each value that was read has gone into
+    // a store, which was issued before this barrier's arrival): shared memory
+    // may change, or go.
     if (ks > 1)
       cluster_sync_relaxed();
     else
