@@ -73,7 +73,6 @@ struct RowPlan {
   static constexpr int kRing = 3;  // stages of a warp's ring
   // buffers of x: with 64 rows there is room for one only
   static constexpr int kXBufs = NT == 64 ? 1 : 2;
-  static constexpr bool kOwnSums = NT <= 32;  // of a stage
   static constexpr int kScaleRow = FMT == TQ_FMT_MX4 ? 8 : 16;  // per stage
   static constexpr int kScalePitch = FMT == TQ_FMT_MX4 ? 16 : 32;
   static constexpr int kCodes = 16 * kStageK / 2;
@@ -537,13 +536,19 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
         // The tensor core cuts its sums instead of rounding them, so a stage
         // has sums of its own, which are added to the others with rounding.
         // NV4, 5376 x 21504: 1.2e-7 off instead of 1.2e-6, in the same time at
-        // 4 and 12 rows, in 55 instead of 51 us at 24. For 64 rows there are
-        // not the registers, and only short sums come there.
-        float own[kTiles][4];
-        auto &sum = P::kOwnSums ? own : acc;
-        if constexpr (P::kOwnSums) {
+        // 4 and 12 rows, in 55 instead of 51 us at 24. 64 rows have not the
+        // registers: there the sums are those of half a stage and four column
+        // tiles at a time, with the half's weights decoded before (83 instead
+        // of 76 us; with a stage's sums of all tiles spilled 85, with one tile
+        // at a time 82 and, 128 experts of 768 x 2048 at 4096 rows, 154 instead
+        // of 147).
+        constexpr bool kStageSums = NT <= 32;
+        constexpr int kWords = kStageSums ? 1 : 4;  // decoded at once
+        constexpr int kAtOnce = kStageSums ? kTiles : 4;  // column tiles
+        float own[kAtOnce][4];
+        if constexpr (kStageSums) {
 #pragma unroll
-          for (int c = 0; c < kTiles; ++c)
+          for (int c = 0; c < kAtOnce; ++c)
 #pragma unroll
             for (int j = 0; j < 4; ++j) own[c][j] = 0.0f;
         }
@@ -556,21 +561,41 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
           const uint32_t w0[4] = {c0.x, c0.y, c0.z, c0.w};
           const uint32_t w1[4] = {c1.x, c1.y, c1.z, c1.w};
 #pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            uint32_t p[4], q[4];
-            f4x8_to_h2(w0[s], p);
-            f4x8_to_h2(w1[s], q);
+          for (int s0 = 0; s0 < 4; s0 += kWords) {
+            uint32_t p[kWords][4], q[kWords][4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              p[c] = hmul2(p[c], f[0][0][s >> 1]);
-              q[c] = hmul2(q[c], f[0][1][s >> 1]);
+            for (int s = 0; s < kWords; ++s) {
+              f4x8_to_h2(w0[s0 + s], p[s]);
+              f4x8_to_h2(w1[s0 + s], q[s]);
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                p[s][c] = hmul2(p[s][c], f[0][0][(s0 + s) >> 1]);
+                q[s][c] = hmul2(q[s][c], f[0][1][(s0 + s) >> 1]);
+              }
             }
 #pragma unroll
-            for (int c = 0; c < kTiles; ++c) {
-              const uint4 v =
-                  lds128(xat + 256 * h + 8 * c * P::kXPitch + 64 * s);
-              mma_f16(sum[c], p[0], q[0], p[1], q[1], v.x, v.y);
-              mma_f16(sum[c], p[2], q[2], p[3], q[3], v.z, v.w);
+            for (int tile = 0; tile < kTiles; tile += kAtOnce) {
+              if constexpr (!kStageSums) {
+#pragma unroll
+                for (int c = 0; c < kAtOnce; ++c)
+                  own[c][0] = own[c][1] = own[c][2] = own[c][3] = 0.0f;
+              }
+#pragma unroll
+              for (int s = 0; s < kWords; ++s)
+#pragma unroll
+                for (int c = 0; c < kAtOnce; ++c) {
+                  const uint4 v =
+                      lds128(xat + 256 * h + 8 * (tile + c) * P::kXPitch +
+                             64 * (s0 + s));
+                  mma_f16(own[c], p[s][0], q[s][0], p[s][1], q[s][1], v.x, v.y);
+                  mma_f16(own[c], p[s][2], q[s][2], p[s][3], q[s][3], v.z, v.w);
+                }
+              if constexpr (!kStageSums) {
+#pragma unroll
+                for (int c = 0; c < kAtOnce; ++c)
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) acc[tile + c][j] += own[c][j];
+              }
             }
           }
 #pragma unroll
@@ -578,7 +603,7 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
 #pragma unroll
             for (int c = 0; c < 2; ++c) f[0][r][c] = f[1][r][c];
         }
-        if constexpr (P::kOwnSums) {
+        if constexpr (kStageSums) {
 #pragma unroll
           for (int c = 0; c < kTiles; ++c)
 #pragma unroll

@@ -7,7 +7,7 @@ import torch
 
 from tests import f4_util as F
 from tests import gpu_util as U
-from tests.test_gpu_f4 import (MX4, NV4, exact_package, gen, integers,
+from tests.test_gpu_f4 import (FMTS, MX4, NV4, exact_package, gen, integers,
                                linear_ws, run_linear, weights)
 
 pytestmark = pytest.mark.gpu
@@ -213,3 +213,30 @@ def test_product_tensor_scales(n, k, b, gw, gx, s):
         U.tq().tq_linear_f4(w, x, y)
         torch.cuda.synchronize()
         assert torch.equal(y, ref.to(dtype))
+
+
+# ---- long sums -----------------------------------------------------------------------
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("b", [5, 16, 32, 64])
+def test_long_sums_of_one_sign(fmt, b):
+    """K = 21504 in one CTA (the GPU is full without a split of K), all terms
+    positive, so that sums which are cut instead of rounded show up.
+
+    A tensor core chains at most 16 products of 16 k, cut at 2^-23 of their
+    sum each; then K / 128 or fewer additions in fp32 follow, off by 2^-24 of
+    the sum each, and a few roundings at the end. x is held to 2^-31 of its
+    row's largest, which is less than all of these."""
+    n, k = 21504, 21504
+    packed = torch.randint(0, 256, (n, k // 2), generator=gen(1),
+                           device=U.DEV, dtype=torch.uint8) & 0x77
+    scales = torch.full((n, k // F.BLOCK[fmt]), 127 if fmt == MX4 else 0x38,
+                        dtype=torch.uint8, device=U.DEV)
+    w = weights(fmt, packed, scales)
+    x = torch.randn(b, k, generator=gen(2), device=U.DEV).abs().bfloat16()
+    y = plain_linear(w, x)
+    rows = torch.arange(0, n, 83, device=U.DEV)
+    w64 = F.values(F.unpack_codes(packed[rows]), scales[rows], fmt)
+    ref = x.double() @ w64.t()
+    err = ((y[:, rows].double() - ref) / ref).abs().max().item()
+    assert err <= (2 * 16 + k // 128 + 4) * 2.0 ** -24, err
