@@ -277,6 +277,15 @@ tq_status tq_unpack(const tq_weights *w, void *W_bf16_out, int32_t *dev_status,
  * reads a NaN table entry; an invalid Format A byte gives an unspecified
  * finite value. Accuracy: |y - y_exact| <= 2e-3 * ||x_b||_2 * max_k |w[n][k]|
  * where y_exact uses the exact decoded weights.
+ * MX4, NV4: |y - y_exact| is at most (k + 8) 2^-23 sum_k |w x| (fp32 sums,
+ * which tensor cores may cut) plus what small values of x lose beside large
+ * ones, sum_k |w[n][k] d[b][k]|. Where x is written as digits (up to 4 rows,
+ * experts with no more rows than experts, tq_linear_ws with a workspace) d is 0
+ * for values of at least 2^-15 of the largest of their block (32 or 16
+ * columns), and else at most 2^-23 of that, or 2^-40 of the row's largest if
+ * that is more. Elsewhere d is 0 down to 2^-31 of the row's largest value, and
+ * else at most 2^-39 of that; MX4 block scales more than 2^131 below the
+ * largest of their row count as 2^131 below.
  * Format A reads: a row's codes and scales are fetched in whole 16-byte
  * blocks, from the block holding the first byte to the block holding the
  * last. A 16-byte block never crosses a page, so these reads stay in mapped
@@ -288,8 +297,8 @@ tq_status tq_linear(const tq_weights *w, const void *x_bf16, int64_t batch,
 
 /* tq_linear with scratch memory of the caller: 4-bit weights and larger
  * batches run on the block-scaled tensor cores, with x written there as 4-bit
- * digits first (same accuracy). tq_linear_workspace says how many bytes help
- * (0: none do, or invalid arguments; host only).
+ * digits first (accuracy: see tq_linear). tq_linear_workspace says how many
+ * bytes help (0: none do, or invalid arguments; host only).
  *   workspace  device, 256-byte aligned, workspace_bytes long, or NULL; with
  *              NULL or too few bytes the call is tq_linear. Its contents are
  *              undefined afterwards; calls that share one must be ordered (on

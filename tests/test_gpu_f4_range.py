@@ -215,6 +215,155 @@ def test_product_tensor_scales(n, k, b, gw, gx, s):
         assert torch.equal(y, ref.to(dtype))
 
 
+# ---- digits ------------------------------------------------------------------------
+
+def digit_x(fmt, b, k, seed):
+    """In every block one 1 where the weight is 0, and values that are integers
+    in 2^-22 down to 2^-20 of it: all 8 digits of base 8 occur."""
+    size = F.BLOCK[fmt]
+    e = torch.randint(5, 21, (b, k), generator=gen(seed), device=U.DEV)
+    m = torch.randint(-7, 8, (b, k), generator=gen(seed + 1), device=U.DEV)
+    here = torch.rand(b, k, generator=gen(seed + 2), device=U.DEV) < 60.0 / k
+    few = torch.rand(b, k, generator=gen(seed + 3), device=U.DEV) < 0.1
+    x = torch.where(few | (e > 14), m, 0) * torch.exp2(-e.float())
+    x = torch.where(here | (e > 16), x, torch.zeros_like(x))
+    x[:, 7::size] = 1.0
+    return x.bfloat16()
+
+
+def digit_package(fmt, n, k, seed):
+    """Weights 0, 1, -1 with unit scales, 0 in column 7 of every block."""
+    size = F.BLOCK[fmt]
+    pick = torch.tensor([0, 2, 10], dtype=torch.uint8, device=U.DEV)
+    codes = pick[torch.randint(0, 3, (n, k), generator=gen(seed),
+                               device=U.DEV)]
+    codes[:, 7::size] = 0
+    scales = torch.full((n, k // size), 127 if fmt == MX4 else 0x38,
+                        dtype=torch.uint8, device=U.DEV)
+    return codes, scales
+
+
+def check_exactness(fmt, codes, scales, x):
+    """The sums of magnitudes stay below 2^24 units of 2^-22."""
+    w64 = F.values(codes, scales, fmt)
+    assert (x.double().abs() @ w64.abs().t()).max() < 4.0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_every_digit(fmt):
+    """Digits made on the spot: up to 4 rows, and experts."""
+    n, k, E = 130, 1056, 16
+    codes, scales = digit_package(fmt, n * E, k, 1)
+    w64 = F.values(codes, scales, fmt)
+    w = weights(fmt, F.pack(codes), scales, None)
+    for b in (1, 2, 3, 4, 7, 20, 64):
+        x = digit_x(fmt, b, k, b)
+        check_exactness(fmt, codes, scales, x)
+        same(run_linear(w, x), x.double() @ w64.t(), f"{b} rows")
+    we = weights(fmt, F.pack(codes), scales, None, n, k)
+    for t in (1, 9, E, 3 * E):
+        x, ids = digit_x(fmt, t, k, t), expert_ids(t, E)
+        same(run_experts(we, E, ids, x), expert_ref(w64, ids, x, n),
+             f"{t} expert rows")
+
+
+@pytest.mark.parametrize("fmt,n,k,batches", [
+    (MX4, 4096, 8192, (3, 5, 8, 9, 20)), (NV4, 16400, 4128, (3, 8, 13)),
+    (MX4, 2080, 4128, (33, 130)), (NV4, 2080, 4128, (40,)),
+    (MX4, 1100, 1952, (600,)), (NV4, 1100, 1952, (513,))])
+def test_every_digit_row(fmt, n, k, batches):
+    """Digits written to a workspace, on both sides of 64 digit rows."""
+    codes, scales = digit_package(fmt, n, k, 2)
+    w64 = F.values(codes, scales, fmt)
+    w = weights(fmt, F.pack(codes), scales, None)
+    for b in batches:
+        x = digit_x(fmt, b, k, b)
+        check_exactness(fmt, codes, scales, x)
+        same(linear_ws(w, x), x.double() @ w64.t(), f"{b} rows")
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("n,k,b", [(4096, 8192, 4), (2080, 4128, 40),
+                                   (16400, 4128, 7), (300, 1056, 2)])
+def test_integers_of_8_bits(fmt, n, k, b):
+    """x of 8 significant bits times 0, 1, -1."""
+    codes, scales = digit_package(fmt, n, k, 3)
+    x = integers(b, k, 4, top=255)
+    y = run_linear(weights(fmt, F.pack(codes), scales, None), x)
+    same(y, x.double() @ F.values(codes, scales, fmt).t(), "8 bits")
+
+
+def value_bound(fmt, w, x, k):
+    """Bound on |y - y_exact| as include/tq.h states it: k additions, each off
+    by at most 2^-23 of the sum of magnitudes, and x off by at most 2^-23 of
+    the largest value of its block or 2^-39 of its row's."""
+    size, ax, aw = F.BLOCK[fmt], x.abs(), w.abs()
+    top = ax.view(x.shape[0], -1, size).amax(2)
+    sums = aw.view(w.shape[0], -1, size).sum(2)
+    return (k + 8) * 2.0 ** -23 * (ax @ aw.t()) + \
+        2.0 ** -23 * (top @ sums.t()) + \
+        2.0 ** -39 * ax.amax(1)[:, None] * aw.sum(1)[None, :] + 1e-37
+
+
+def far_below(fmt, b, k, seed, low):
+    """In column 7 of every block a large value (weight 0), the others 2^-16 to
+    2^-low of it: what they lose shows."""
+    e = torch.randint(16, low + 1, (b, k), generator=gen(seed), device=U.DEV)
+    m = 1 + torch.rand(b, k, generator=gen(seed + 1), device=U.DEV)
+    x = m * torch.exp2(-e.float())
+    x[:, 7::F.BLOCK[fmt]] = 1.0
+    x[:, 1::3] *= -1
+    return x.bfloat16()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("low", [20, 30, 45])
+def test_values_far_below_their_block(fmt, low):
+    n, k, E = 130, 1056, 16
+    codes, scales = digit_package(fmt, n * E, k, 4)
+    w64 = F.values(codes, scales, fmt)
+    w = weights(fmt, F.pack(codes), scales, None)
+    for b in BATCHES:
+        x = far_below(fmt, b, k, b, low)
+        F.check(run_linear(w, x), x.double() @ w64.t(),
+                value_bound(fmt, w64, x.double(), k), f"{b} rows")
+    we = weights(fmt, F.pack(codes), scales, None, n, k)
+    x, ids = far_below(fmt, E, k, 3, low), expert_ids(E, E)
+    tol = value_bound(fmt, w64, x.double(), k).view(E, E, n)
+    F.check(run_experts(we, E, ids, x), expert_ref(w64, ids, x, n),
+            tol[torch.arange(E, device=U.DEV), ids.long()], "experts")
+
+
+@pytest.mark.parametrize("fmt,n,k,b", [(MX4, 4096, 8192, 5),
+                                       (MX4, 2080, 4128, 40),
+                                       (NV4, 16400, 4128, 5),
+                                       (NV4, 2080, 4128, 40)])
+def test_digit_rows_far_below_their_block(fmt, n, k, b):
+    codes, scales = digit_package(fmt, n, k, 5)
+    w64 = F.values(codes, scales, fmt)
+    w = weights(fmt, F.pack(codes), scales, None)
+    for low in (20, 45):
+        x = far_below(fmt, b, k, b, low)
+        F.check(linear_ws(w, x), x.double() @ w64.t(),
+                value_bound(fmt, w64, x.double(), k), f"2^-{low}")
+
+
+def test_ones_beside_the_smallest():
+    """x = (1, then values just below 2^-23), the 1 at weight 0: half of the
+    sum may be lost to the digits, and no more."""
+    k = 32
+    codes = torch.full((4, k), 7, dtype=torch.uint8, device=U.DEV)  # 6
+    codes[:, 0] = 0
+    scales = torch.full((4, 1), 127, dtype=torch.uint8, device=U.DEV)
+    w64 = F.values(codes, scales, MX4)
+    for b in (1, 5):
+        x = torch.full((b, k), 1.9921875 * 2.0 ** -24, device=U.DEV)
+        x[:, 0] = 1.0
+        x = x.bfloat16()
+        F.check(run_linear(weights(MX4, F.pack(codes), scales), x),
+                x.double() @ w64.t(), value_bound(MX4, w64, x.double(), k))
+
+
 # ---- long sums -----------------------------------------------------------------------
 
 @pytest.mark.parametrize("fmt", FMTS)
