@@ -348,6 +348,14 @@ def _weights_f4(fmt, codes, scales, lut, n, k) -> Weights:
     if n is None:
         n, k = codes.shape[0], codes.shape[1] * 2
     _f4_stacked(fmt, codes, scales, lut, 1, n, k, "weights")
+    device = codes.get_device()
+    for t, types, what in ((codes, _U8, "codes"), (scales, _U8, "scales"),
+                           (lut, _F32, "tensor scale")):
+        if t is not None and (t.dtype not in types or
+                              not t.is_contiguous() or
+                              t.get_device() != device):
+            raise TqError(TQ_ERR_INVALID_ARG, f"weights: {what} {t.dtype}, "
+                          f"strides {t.stride()}, on {t.device}")
     d = tq_weights(format=fmt, group=F4_BLOCK[fmt], planes=1,
                    rows_per_scale=0, n_rows=n, k_cols=k, codes=_ptr(codes),
                    scales=_ptr(scales), lut=_ptr(lut), codes_plane_stride=0,
@@ -357,8 +365,8 @@ def _weights_f4(fmt, codes, scales, lut, n, k) -> Weights:
 
 def weights_mx4(codes, scales, n=None, k=None) -> Weights:
     """4-bit floats, blocks of 32: codes [n][k/2] (low four bits = lower k),
-    E8M0 scale bytes [n][k/32]. For tq_linear_experts_f4: the stacked experts,
-    n the rows of one."""
+    E8M0 scale bytes [n][k/32], both dense. For tq_linear_experts_f4: the
+    stacked experts, n the rows of one."""
     return _weights_f4(TQ_FMT_MX4, codes, scales, None, n, k)
 
 
