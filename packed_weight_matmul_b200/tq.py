@@ -348,12 +348,11 @@ def _weights_f4(fmt, codes, scales, lut, n, k) -> Weights:
     if n is None:
         n, k = codes.shape[0], codes.shape[1] * 2
     _f4_stacked(fmt, codes, scales, lut, 1, n, k, "weights")
-    device = codes.get_device()
     for t, types, what in ((codes, _U8, "codes"), (scales, _U8, "scales"),
                            (lut, _F32, "tensor scale")):
         if t is not None and (t.dtype not in types or
                               not t.is_contiguous() or
-                              t.get_device() != device):
+                              t.device != codes.device):
             raise TqError(TQ_ERR_INVALID_ARG, f"weights: {what} {t.dtype}, "
                           f"strides {t.stride()}, on {t.device}")
     d = tq_weights(format=fmt, group=F4_BLOCK[fmt], planes=1,
