@@ -130,10 +130,12 @@ def _ptr(t):
     return t.data_ptr()
 
 
-def _stream(stream):
+def _stream(stream, device=None):
+    """`device`: the current one, where the caller knows it."""
     if stream is None:
         # torch.cuda.current_stream().cuda_stream without the object (2 us)
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return torch._C._cuda_getCurrentRawStream(
+            torch._C._cuda_getDevice() if device is None else device)
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return stream
@@ -262,9 +264,24 @@ def tq_status_string(status: int) -> str:
 class Weights:
     """A tq_weights descriptor that keeps its tensors alive."""
 
-    def __init__(self, desc: tq_weights, keep):
+    def __init__(self, desc: tq_weights, keep, device=None):
         self.desc = desc
+        self.ref = C.byref(desc)
         self._keep = keep
+        # 4-bit formats: device number (-1 on the host), sizes as plain numbers
+        # and bytes of workspace by batch (attributes of a ctypes structure and
+        # calls through ctypes take several times as long)
+        self.device = device
+        self.shape = (desc.n_rows, desc.k_cols)
+        self._workspaces = {}
+
+    def workspace(self, batch):
+        """tq_linear_workspace."""
+        need = self._workspaces.get(batch)
+        if need is None:
+            need = _lib.tq_linear_workspace(self.ref, batch)
+            self._workspaces[batch] = need
+        return need
 
     @property
     def n(self):
@@ -359,7 +376,7 @@ def _weights_f4(fmt, codes, scales, lut, n, k) -> Weights:
                    rows_per_scale=0, n_rows=n, k_cols=k, codes=_ptr(codes),
                    scales=_ptr(scales), lut=_ptr(lut), codes_plane_stride=0,
                    scales_plane_stride=0, lut_rows=0)
-    return Weights(d, (codes, scales, lut))
+    return Weights(d, (codes, scales, lut), codes.get_device())
 
 
 def weights_mx4(codes, scales, n=None, k=None) -> Weights:
@@ -410,8 +427,18 @@ def tq_encode_b(W, ladder, zeta, rows_per_scale, codes_out, rho_out,
 
 
 def tq_unpack(w: Weights, out, dev_status=None, stream=None, check=True):
-    st = _lib.tq_unpack(C.byref(w.desc), _ptr(out), _ptr(dev_status),
-                        _stream(stream))
+    if w.device is not None:
+        n, k = w.shape
+        dev = w.device
+        if not (dev >= 0 and dev == torch._C._cuda_getDevice() and
+                _f4_plain(out, torch.bfloat16, dev, n * k)):
+            _f4_operands(w, ((out, _BF16, 1, 0, n * k),), "tq_unpack")
+            if not (isinstance(out, int) or out.is_contiguous()):
+                raise TqError(TQ_ERR_INVALID_ARG, "tq_unpack: not dense")
+        if dev_status is not None:
+            _f4_status(dev_status, dev, "tq_unpack: dev_status")
+    st = _lib.tq_unpack(w.ref, _ptr(out), _ptr(dev_status),
+                        _stream(stream, w.device))
     if check:
         _check(st, "tq_unpack")
     return st
@@ -426,18 +453,25 @@ def tq_linear(w: Weights, x, y, batch=None, ldx=None, ldy=None, stream=None,
     if ldy is None:
         ldy = y.stride(0) if y.dim() == 2 else w.n
     need = 0
-    if w.desc.format in F4_BLOCK:
-        need = _lib.tq_linear_workspace(C.byref(w.desc), batch)
+    if w.device is not None:
+        n, k = w.shape
+        dev = w.device
+        if not (dev >= 0 and dev == torch._C._cuda_getDevice() and
+                _f4_plain(x, torch.bfloat16, dev, (batch - 1) * ldx + k) and
+                _f4_plain(y, torch.float32, dev, (batch - 1) * ldy + n)):
+            _f4_operands(w, ((x, _BF16, batch, ldx, k),
+                             (y, _F32, batch, ldy, n)), "tq_linear")
+        need = w.workspace(batch)
     if need:
         # scratch from torch's allocator, on the stream that uses it
         with _torch_stream(stream):
             ws = torch.empty(need, dtype=torch.uint8, device="cuda")
-            st = _lib.tq_linear_ws(C.byref(w.desc), _ptr(x), batch, ldx,
+            st = _lib.tq_linear_ws(w.ref, _ptr(x), batch, ldx,
                                    _ptr(y), ldy, ws.data_ptr(), need,
                                    _stream(None))
     else:
-        st = _lib.tq_linear(C.byref(w.desc), _ptr(x), batch, ldx, _ptr(y), ldy,
-                            _stream(stream))
+        st = _lib.tq_linear(w.ref, _ptr(x), batch, ldx, _ptr(y), ldy,
+                            _stream(stream, w.device))
     if check:
         _check(st, "tq_linear")
     return st
@@ -451,16 +485,58 @@ def _f4_device(t, what):
     return dev
 
 
-def _f4_tensor(t, dtypes, dev, what):
+def _f4_types(t, dtypes, what):
     """The 4-bit entry points check what the C ABI cannot see of a tensor:
-    that it lies on the current device, with the element type it is read as
-    and dense rows."""
-    if t.get_device() != dev:
-        raise TqError(TQ_ERR_INVALID_ARG, f"{what}: not on the current device")
+    that it has the element type it is read as and dense rows, and (see the
+    callers) that it is large enough and lies on the current device."""
     if t.dtype not in dtypes:
         raise TqError(TQ_ERR_INVALID_ARG, f"{what}: {t.dtype}")
     if not t.is_contiguous() and t.stride(-1) != 1 and t.shape[-1] > 1:
         raise TqError(TQ_ERR_INVALID_ARG, f"{what}: rows are not dense")
+
+
+def _f4_tensor(t, dtypes, dev, what):
+    _f4_types(t, dtypes, what)
+    if t.get_device() != dev:
+        raise TqError(TQ_ERR_INVALID_ARG, f"{what}: not on the current device")
+
+
+def _f4_plain(t, dtype, dev, count):
+    """The common case in few steps: dense, `count` elements at least."""
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and
+            t.is_contiguous() and t.numel() >= count and
+            t.get_device() == dev)
+
+
+def _f4_operands(w, operands, what):
+    """(tensor, element types, rows, distance of the rows, columns) each: the
+    rows have to lie within the tensor. Plain pointers are taken as they
+    are."""
+    tensors = [o for o in operands if not isinstance(o[0], int)]
+    for t, _, rows, ld, cols in tensors:
+        have = t.numel()
+        if have and not t.is_contiguous():
+            have = 1 + sum((s - 1) * d for s, d in zip(t.shape, t.stride()))
+        if cols and rows > 0 and have < (rows - 1) * ld + cols:
+            raise TqError(TQ_ERR_SHAPE, f"{what}: {tuple(t.shape)}")
+    for t, dtypes, _, _, _ in tensors:
+        _f4_types(t, dtypes, what)
+    for t, _, _, _, _ in tensors:
+        _f4_device(t, what)
+    if w.device < 0 or w.device != torch._C._cuda_getDevice():
+        raise TqError(TQ_ERR_INVALID_ARG,
+                      f"{what}: weights not on the current device")
+
+
+def _f4_package(w, dev, what):
+    """Whether the package lies on the device (other formats: not known)."""
+    if w.device is not None and w.device != dev:
+        raise TqError(TQ_ERR_INVALID_ARG, f"{what}: not on the current device")
+
+
+def _f4_status(t, dev, what):
+    if isinstance(t, torch.Tensor):
+        _f4_tensor(t, (torch.int32,), dev, what)
 
 
 def _rows(t):
@@ -481,19 +557,24 @@ def tq_quantize_f4(W, fmt, codes_out, scales_out, tensor_scale=None,
     written."""
     n, k = W.shape
     dev = _f4_device(W, "tq_quantize_f4: W")
-    _f4_tensor(W, _BF16, dev, "tq_quantize_f4: W")
-    _f4_tensor(codes_out, _U8, dev, "tq_quantize_f4: codes_out")
-    _f4_tensor(scales_out, _U8, dev, "tq_quantize_f4: scales_out")
-    if codes_out.numel() * 2 < n * k or not codes_out.is_contiguous() or \
-            scales_out.numel() * F4_BLOCK.get(fmt, 16) < n * k or \
-            not scales_out.is_contiguous():
-        raise TqError(TQ_ERR_SHAPE, "tq_quantize_f4: outputs")
+    if not _f4_plain(W, torch.bfloat16, dev, 0):
+        _f4_tensor(W, _BF16, dev, "tq_quantize_f4: W")
+    blocks = n * k // F4_BLOCK.get(fmt, 16)
+    if not (_f4_plain(codes_out, torch.uint8, dev, n * k // 2) and
+            _f4_plain(scales_out, torch.uint8, dev, blocks)):
+        _f4_tensor(codes_out, _U8, dev, "tq_quantize_f4: codes_out")
+        _f4_tensor(scales_out, _U8, dev, "tq_quantize_f4: scales_out")
+        if codes_out.numel() * 2 < n * k or scales_out.numel() < blocks or \
+                not (codes_out.is_contiguous() and scales_out.is_contiguous()):
+            raise TqError(TQ_ERR_SHAPE, "tq_quantize_f4: outputs")
     if tensor_scale is not None:
         _f4_tensor(tensor_scale, _F32, dev, "tq_quantize_f4: scale")
+    if dev_status is not None:
+        _f4_status(dev_status, dev, "tq_quantize_f4: dev_status")
     st = _lib.tq_quantize_f4(W.data_ptr(), n, k, _rows(W), fmt,
                              codes_out.data_ptr(), scales_out.data_ptr(),
                              _ptr(tensor_scale), int(bool(scale_given)),
-                             _ptr(dev_status), _stream(stream))
+                             _ptr(dev_status), _stream(stream, dev))
     if check:
         _check(st, "tq_quantize_f4")
     return st
@@ -502,13 +583,15 @@ def tq_quantize_f4(W, fmt, codes_out, scales_out, tensor_scale=None,
 def tq_linear_f4(w: Weights, x: Weights, y, stream=None, check=True):
     """y = x W^T of two 4-bit matrices of one format; y fp32 or bf16
     [batch][n], row stride free."""
-    _f4_tensor(y, _BF16 + _F32, _f4_device(y, "tq_linear_f4: y"),
-               "tq_linear_f4: y")
+    dev = _f4_device(y, "tq_linear_f4: y")
+    _f4_tensor(y, _BF16 + _F32, dev, "tq_linear_f4: y")
+    _f4_package(w, dev, "tq_linear_f4: w")
+    _f4_package(x, dev, "tq_linear_f4: x")
     if y.dim() != 2 or y.shape[0] < x.n or y.shape[1] < w.n:
         raise TqError(TQ_ERR_SHAPE, "tq_linear_f4: y")
-    st = _lib.tq_linear_f4(C.byref(w.desc), C.byref(x.desc), y.data_ptr(),
+    st = _lib.tq_linear_f4(w.ref, x.ref, y.data_ptr(),
                            _rows(y), TQ_Y_BF16 if y.dtype == torch.bfloat16
-                           else TQ_Y_F32, _stream(stream))
+                           else TQ_Y_F32, _stream(stream, dev))
     if check:
         _check(st, "tq_linear_f4")
     return st
@@ -522,6 +605,9 @@ def tq_linear_experts_f4(w: Weights, n_experts, ids, x, y, status=None,
     _f4_tensor(ids, (torch.int32,), dev, "tq_linear_experts_f4: ids")
     _f4_tensor(x, _BF16, dev, "tq_linear_experts_f4: x")
     _f4_tensor(y, _F32, dev, "tq_linear_experts_f4: y")
+    _f4_package(w, dev, "tq_linear_experts_f4: weights")
+    if status is not None:
+        _f4_status(status, dev, "tq_linear_experts_f4: status")
     if ids.dim() != 1 or x.dim() != 2 or y.dim() != 2:
         raise TqError(TQ_ERR_SHAPE, "tq_linear_experts_f4: ids, x, y")
     if w.desc.format in F4_BLOCK:
@@ -531,9 +617,10 @@ def tq_linear_experts_f4(w: Weights, n_experts, ids, x, y, status=None,
     if x.shape[0] < t or y.shape[0] < t or x.shape[1] < w.k or \
             y.shape[1] < w.n:
         raise TqError(TQ_ERR_SHAPE, "tq_linear_experts_f4: x, y")
-    st = _lib.tq_linear_experts_f4(C.byref(w.desc), n_experts, ids.data_ptr(),
+    st = _lib.tq_linear_experts_f4(w.ref, n_experts, ids.data_ptr(),
                                    t, x.data_ptr(), _rows(x), y.data_ptr(),
-                                   _rows(y), _ptr(status), _stream(stream))
+                                   _rows(y), _ptr(status),
+                                   _stream(stream, dev))
     if check:
         _check(st, "tq_linear_experts_f4")
     return st
