@@ -130,12 +130,18 @@ def _ptr(t):
     return t.data_ptr()
 
 
+# torch's own functions behind current_stream and current_device, which take 2
+# us less per call; the public ones where torch has them no longer.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or \
+    torch.cuda.current_device
+
+
 def _stream(stream, device=None):
     """`device`: the current one, where the caller knows it."""
     if stream is None:
-        # torch.cuda.current_stream().cuda_stream without the object (2 us)
-        return torch._C._cuda_getCurrentRawStream(
-            torch._C._cuda_getDevice() if device is None else device)
+        return _raw_stream(_current_device() if device is None else device)
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return stream
@@ -430,7 +436,7 @@ def tq_unpack(w: Weights, out, dev_status=None, stream=None, check=True):
     if w.device is not None:
         n, k = w.shape
         dev = w.device
-        if not (dev >= 0 and dev == torch._C._cuda_getDevice() and
+        if not (dev >= 0 and dev == _current_device() and
                 _f4_plain(out, torch.bfloat16, dev, n * k)):
             _f4_operands(w, ((out, _BF16, 1, 0, n * k),), "tq_unpack")
             if not (isinstance(out, int) or out.is_contiguous()):
@@ -456,7 +462,7 @@ def tq_linear(w: Weights, x, y, batch=None, ldx=None, ldy=None, stream=None,
     if w.device is not None:
         n, k = w.shape
         dev = w.device
-        if not (dev >= 0 and dev == torch._C._cuda_getDevice() and
+        if not (dev >= 0 and dev == _current_device() and
                 _f4_plain(x, torch.bfloat16, dev, (batch - 1) * ldx + k) and
                 _f4_plain(y, torch.float32, dev, (batch - 1) * ldy + n)):
             _f4_operands(w, ((x, _BF16, batch, ldx, k),
@@ -480,7 +486,7 @@ def tq_linear(w: Weights, x, y, batch=None, ldx=None, ldy=None, stream=None,
 def _f4_device(t, what):
     """The current device, on which t has to lie."""
     dev = t.get_device()
-    if dev < 0 or dev != torch._C._cuda_getDevice():
+    if dev < 0 or dev != _current_device():
         raise TqError(TQ_ERR_INVALID_ARG, f"{what}: not on the current device")
     return dev
 
@@ -523,7 +529,7 @@ def _f4_operands(w, operands, what):
         _f4_types(t, dtypes, what)
     for t, _, _, _, _ in tensors:
         _f4_device(t, what)
-    if w.device < 0 or w.device != torch._C._cuda_getDevice():
+    if w.device < 0 or w.device != _current_device():
         raise TqError(TQ_ERR_INVALID_ARG,
                       f"{what}: weights not on the current device")
 

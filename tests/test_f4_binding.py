@@ -150,3 +150,15 @@ def test_calls_refuse_host_tensors_beside_device_ones(tq):
     out.fill_(7.0)
     tq.tq_unpack(w, out)
     assert (out == 0).all()
+
+
+@pytest.mark.gpu
+def test_stream_is_torchs_current_one(tq):
+    torch.zeros(1, device="cuda:0")
+    side = torch.cuda.Stream()
+    for device in (None, torch.cuda.current_device()):
+        assert tq._stream(None, device) == \
+            torch.cuda.current_stream().cuda_stream
+        with torch.cuda.stream(side):
+            assert tq._stream(None, device) == side.cuda_stream
+    assert tq._stream(side) == side.cuda_stream and tq._stream(7) == 7
