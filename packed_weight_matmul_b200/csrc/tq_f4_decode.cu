@@ -12,8 +12,8 @@
 //
 // Bound by the codes' way from HBM: an MMA of 64 k takes 41 to 64 cycles for
 // 8192 weights, 2 to 3 times the rate at which HBM delivers them. A digit
-// costs 3 lane instructions per value of x and CTA, so the kernel takes 16
-// rows of x at most. MX4, 8192 x 5376: 1 row 10.0 us, 16 packed rows 8.9 us
+// costs 3 lane instructions per value of x and CTA, so a pass takes 4 bf16
+// rows (packed ones: 32 or 64). MX4, 8192 x 5376: 1 row 10.0 us, 16 packed rows 8.9 us
 // (HBM alone 3.6; 5 us are start-up and the sum over the cluster); 21504 x
 // 5376, 1 row: 16.5 us, 3.7 TB/s; 64 rows over 128 experts of 768 x 2048: 18
 // us.
@@ -81,7 +81,7 @@ struct DecodePlan {
   static constexpr uint32_t kSmem = kOffBar + 256 + 1024;
   static constexpr int kPitch = kTile + 4;  // of the partial tile
   static_assert(kRows * kPitch * 4 <= kOffS, "partial tile");
-  static_assert(SRC == kPacked || kRows <= 16, "rows per warp");
+  static_assert(SRC == kPacked || kRows == 4, "rows that share a stage");
 };
 
 struct DecodeArgs {
@@ -166,10 +166,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   // `rows` rows of x (s_rows[first + i], or b0 + i): one pass over K
   auto pass = [&](int pass_no, int first, int64_t b0, int rows) {
     const int64_t wrow = expert * a.n + row0;  // first weight row
-    // Warps that share a stage's rows of x (their arrivals add up to 8), and
-    // stages in work at once: a wait by parity is right one phase ahead, so a
-    // warp skips S stages at most.
-    const int per_stage = rows <= 1 ? 1 : rows <= 2 ? 2 : rows <= 4 ? 4 : 8;
+    // bf16 x: warps that share a stage's rows (their arrivals add up to 8),
+    // one row each, and stages in work at once: a wait by parity is right one
+    // phase ahead, so a warp skips S stages at most.
+    const int per_stage = rows <= 1 ? 1 : rows <= 2 ? 2 : 4;
     const int at_once = 8 / per_stage < S ? 8 / per_stage : S;
     // Scales to tensor memory: group `turn` of four warps.
     auto move_scales = [&](int turn) {
@@ -353,19 +353,14 @@ __global__ void __launch_bounds__(kThreads, 2)
         return a.x + (a.ids != nullptr ? s_rows[first + r] : b0 + r) * a.ldx;
       };
       if constexpr (SRC == kBf16) {
-        constexpr int kStaged = P::kRows > 8 ? 2 : 1;  // rows of a warp
         // the first values to convert, on their way during what follows
-        const int mine = xw % per_stage;
-        uint4 next[kStaged];
+        const int mine = xw % per_stage;  // this warp's row
+        uint4 next;
         auto load = [&](int i) {
           const int64_t k = k0 + (int64_t)i * kStageK + 8 * lane;
-#pragma unroll
-          for (int j = 0; j < kStaged; ++j) {
-            const int r = mine + 8 * j;
-            next[j] = make_uint4(0, 0, 0, 0);
-            if (r < rows && i < steps && k < k1)
-              next[j] = __ldg(reinterpret_cast<const uint4 *>(x_row(r) + k));
-          }
+          next = make_uint4(0, 0, 0, 0);
+          if (mine < rows && i < steps && k < k1)
+            next = __ldg(reinterpret_cast<const uint4 *>(x_row(mine) + k));
         };
         // warps past the last group of per_stage have no stages of their own
         const int start = xw / per_stage < at_once ? xw / per_stage : steps;
@@ -377,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           s_odd[r] = 0;
         }
         bar_sync(2, kXThreads);
-        const int parts = rows < 8 ? 8 / rows : 1;
+        const int parts = 8 / rows;
         for (int u = xw; u < rows * parts; u += 8) {
           const int r = u % rows, part = u / rows;
           const __nv_bfloat16 *p = x_row(r);
@@ -428,36 +423,30 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll 1
         for (; i < steps; i += at_once) {
           const uint32_t it = done + i, s = it % S, ph = (it / S) & 1u;
-          uint4 now[kStaged];
-#pragma unroll
-          for (int j = 0; j < kStaged; ++j) now[j] = next[j];
+          uint4 w = next;
           load(i + at_once);
           bool ok = mbar_wait(empty + 8 * s, ph ^ 1u, abort_addr, kWaitLimitNs);
           ok = __all_sync(0xFFFFFFFFu, ok);
           if (!ok) break;
-#pragma unroll 1
-          for (int j = 0; j < kStaged; ++j) {
-            const int r = mine + 8 * j;
-            if (r >= rows) break;
-            uint4 w = now[0];
-            if (kStaged > 1 && j == 1) w = now[kStaged - 1];
-            if (s_odd[r]) w = only_finite8(w);
+          if (mine < rows) {
+            if (s_odd[mine]) w = only_finite8(w);
             uint32_t m = max_mag8(w);
             m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
             if (FMT == TQ_FMT_MX4)
               m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
             uint32_t byte, field;
-            digit_scale<FMT>(max((int)(m >> 7), 1), s_exp[r], &byte, &field);
+            digit_scale<FMT>(max((int)(m >> 7), 1), s_exp[mine], &byte,
+                             &field);
             constexpr int kLanes = f4_block(FMT) / 8;
             if (lane % kLanes == 0)
               asm volatile("st.shared.u8 [%0], %1;" ::"r"(
-                               base + P::kOffE + s * P::kExp + r * 16 +
+                               base + P::kOffE + s * P::kExp + mine * 16 +
                                lane / kLanes),
                            "r"(byte)
                            : "memory");
-            // row 8 r + i: 16-byte chunk c (32 codes) lies at c ^ i
+            // row 8 mine + i: 16-byte chunk c (32 codes) lies at c ^ i
             const uint32_t at =
-                base + P::kOffB + s * P::kB + r * 1024 + (lane & 3) * 4;
+                base + P::kOffB + s * P::kB + mine * 1024 + (lane & 3) * 4;
             digits8(w, field, [&](int d, uint32_t codes) {
               asm volatile("st.shared.b32 [%0], %1;" ::"r"(
                                at + d * 128 + (((lane >> 2) ^ d) << 4)),
@@ -748,21 +737,13 @@ cudaError_t launch(const WeightsView &w, const WeightsView *x, DecodeArgs a,
   return cudaLaunchKernelEx(&cfg, kern, mw, mx, a);
 }
 
-template <int SRC>
-cudaError_t launch_nt(const WeightsView &w, const WeightsView *x, int nt,
-                      const DecodeArgs &a, int64_t copies, int64_t grid_y,
-                      cudaStream_t stream) {
-  const bool mx = w.format == TQ_FMT_MX4;
-  if (nt == 32)
-    return mx ? launch<TQ_FMT_MX4, 32, SRC>(w, x, a, copies, grid_y, stream)
-              : launch<TQ_FMT_NV4, 32, SRC>(w, x, a, copies, grid_y, stream);
-  if (nt == 64)
-    return mx ? launch<TQ_FMT_MX4, 64, SRC>(w, x, a, copies, grid_y, stream)
-              : launch<TQ_FMT_NV4, 64, SRC>(w, x, a, copies, grid_y, stream);
-  if constexpr (SRC == kBf16)
-    return mx ? launch<TQ_FMT_MX4, 128, SRC>(w, x, a, copies, grid_y, stream)
-              : launch<TQ_FMT_NV4, 128, SRC>(w, x, a, copies, grid_y, stream);
-  return cudaErrorInvalidValue;
+template <int NT, int SRC>
+cudaError_t launch_format(const WeightsView &w, const WeightsView *x,
+                          const DecodeArgs &a, int64_t copies, int64_t grid_y,
+                          cudaStream_t stream) {
+  return w.format == TQ_FMT_MX4
+             ? launch<TQ_FMT_MX4, NT, SRC>(w, x, a, copies, grid_y, stream)
+             : launch<TQ_FMT_NV4, NT, SRC>(w, x, a, copies, grid_y, stream);
 }
 
 DecodeArgs weight_args(const WeightsView &w) {
@@ -774,8 +755,6 @@ DecodeArgs weight_args(const WeightsView &w) {
   a.k = (int)w.k;
   return a;
 }
-
-int width_for(int64_t rows) { return rows <= 4 ? 32 : rows <= 8 ? 64 : 128; }
 
 }  // namespace
 
@@ -792,9 +771,8 @@ cudaError_t decode_f4_bf16(const WeightsView &w, const __nv_bfloat16 *x,
   a.y = y;
   a.ldy = ldy;
   a.batch = batch;
-  const int nt = width_for(batch);
-  const int64_t passes = (batch + nt / 8 - 1) / (nt / 8);
-  return launch_nt<kBf16>(w, nullptr, nt, a, passes, passes, stream);
+  const int64_t passes = (batch + 3) / 4;
+  return launch_format<32, kBf16>(w, nullptr, a, passes, passes, stream);
 }
 
 cudaError_t decode_f4_experts(const WeightsView &w, int n_experts,
@@ -813,9 +791,7 @@ cudaError_t decode_f4_experts(const WeightsView &w, int n_experts,
   a.status = status;
   const int64_t used = tokens < n_experts ? tokens : n_experts;
   a.slots = n_experts <= kMapExperts ? (int)used : n_experts;
-  return launch_nt<kBf16>(w, nullptr,
-                          width_for(2 * ((tokens + n_experts - 1) / n_experts)),
-                          a, used, a.slots, stream);
+  return launch_format<32, kBf16>(w, nullptr, a, used, a.slots, stream);
 }
 
 cudaError_t decode_f4_packed(const WeightsView &w, const WeightsView &x,
@@ -829,9 +805,8 @@ cudaError_t decode_f4_packed(const WeightsView &w, const WeightsView &x,
   a.ldy = ldy;
   a.y_bf16 = y_type == TQ_Y_BF16;
   a.batch = x.n;
-  const int nt = x.n <= 32 ? 32 : 64;
-  const int64_t passes = (x.n + nt - 1) / nt;
-  return launch_nt<kPacked>(w, &x, nt, a, passes, passes, stream);
+  return x.n <= 32 ? launch_format<32, kPacked>(w, &x, a, 1, 1, stream)
+                   : launch_format<64, kPacked>(w, &x, a, 1, 1, stream);
 }
 
 }  // namespace tq

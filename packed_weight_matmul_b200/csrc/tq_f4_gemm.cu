@@ -11,7 +11,8 @@
 // r / 32, one 32-bit column word per row holding the scales of 128 (MX4) or
 // 64 (NV4) consecutive k.
 //
-// A tile is CG * 128 weight rows (M) times NT batch rows (N); CG = 2 pairs
+// For more than 64 batch rows (fewer: tq_f4_decode.cu). A tile is CG * 128
+// weight rows (M) times NT = 128 or 256 batch rows (N); CG = 2 pairs
 // the CTAs of a cluster on one tile (each holds its 128 weight rows and half
 // of the batch rows). Persistent, 16 (pair, NV4) or 18 warps per CTA:
 //   warp 0       TMA producer: per stage of 256 k the 128-byte swizzled boxes
@@ -562,7 +563,7 @@ __global__ void __launch_bounds__(Plan<FMT, NT, CG>::kThreads, 1)
       // warp instead of 1150). As many columns as 64 registers hold are read first, so that the next
       // tile can start while they are stored: all of them as bf16 pairs (two
       // columns of this lane's row), 64 in fp32.
-      uint32_t h[kCols / 2 < 16 ? 16 : kCols / 2] = {};
+      uint32_t h[kCols / 2] = {};
       if (args.digits.exps != nullptr) {
         const DigitArgs &D = args.digits;
         const float one = ok ? g : __int_as_float(0x7FC00000);
@@ -640,7 +641,7 @@ __global__ void __launch_bounds__(Plan<FMT, NT, CG>::kThreads, 1)
           }
         }
       } else {
-        constexpr int kHeld = kCols / 2 < 16 ? 16 : kCols / 2;
+        constexpr int kHeld = kCols / 2;
         float *p = static_cast<float *>(args.y) + b0 * args.ldy + row;
 #pragma unroll 1
         for (int c = 0; c < kCols; c += kHeld) {
@@ -720,8 +721,6 @@ cudaError_t launch(const WeightsView &w, const WeightsView &x, Args a,
 template <int FMT>
 cudaError_t dispatch(const WeightsView &w, const WeightsView &x, const Args &a,
                      cudaStream_t stream) {
-  if (x.n <= 32) return launch<FMT, 32, 1>(w, x, a, stream);
-  if (x.n <= 64) return launch<FMT, 64, 1>(w, x, a, stream);
   // A wave of 256 x 256 tiles takes about 7/5 of the time of a wave of 128 x
   // 128 tiles, two of which cover half of it, so the large tile wins where its
   // waves are full: MX4 (NV4) 101 (113) against 129 (150) us at 21504 x 5376 x
@@ -763,7 +762,7 @@ cudaError_t product_f4(const WeightsView &w, const WeightsView &x, void *y,
                        cudaStream_t stream) {
   // up to 64 rows the kernel that splits K (8192 x 5376 x 16 rows: 8.6 against
   // 10.8 us); for 128 both take the same
-  if (x.n <= 64 && decode_f4_supported(w, 1))
+  if (x.n <= 64)
     return decode_f4_packed(w, x, y, ldy, y_type, digits, stream);
   Args a = args_of(w, x, y, ldy);
   a.y_bf16 = y_type == TQ_Y_BF16;
