@@ -44,6 +44,25 @@ __device__ __forceinline__ float f4_scale(uint32_t b) {
   return FMT == TQ_FMT_MX4 ? e8m0_to_f32(b) : e4m3_to_f32(b);
 }
 
+// Largest magnitude (bf16 bits) of the 8 values of a 16-byte word.
+__device__ __forceinline__ uint32_t max_mag8(const uint4 &w) {
+  const uint32_t m = __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
+                              __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
+  return max(m >> 16, m & 0xFFFFu);
+}
+
+// The same over the finite values, one by one.
+static __device__ __noinline__ uint32_t max_finite8(uint4 w) {
+  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t a = (v[i >> 1] >> (16 * (i & 1))) & 0x7FFFu;
+    if (a < 0x7F80u) m = max(m, a);
+  }
+  return m;
+}
+
 // A tensor scale g = m 2^e with |m| < 1 (0, NaN and Inf as they are): sums may
 // lie outside of fp32's range where g brings them back, so m is applied first
 // and e together with the other exponents.
@@ -127,7 +146,6 @@ struct DigitArgs;
 cudaError_t decode_f4_packed(const WeightsView &w, const WeightsView &x,
                              void *y, int64_t ldy, int y_type,
                              const f4::DigitArgs &digits, cudaStream_t stream);
-
 
 // tq_linear with a workspace (tq_f4_digits.cu): bytes (0: of no use), call.
 int64_t digits_f4_workspace(const WeightsView &w, int64_t batch);

@@ -26,12 +26,6 @@
 namespace tq {
 namespace f4 {
 
-__device__ __forceinline__ uint32_t max_mag8(const uint4 &w) {
-  const uint32_t m = __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
-                              __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
-  return max(m >> 16, m & 0xFFFFu);
-}
-
 // NaN and Inf become 0.
 __device__ __forceinline__ uint4 only_finite8(uint4 w) {
   uint32_t v[4] = {w.x, w.y, w.z, w.w};

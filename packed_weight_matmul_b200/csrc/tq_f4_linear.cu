@@ -48,8 +48,10 @@ constexpr int kStageK = 256;    // codes of a row per stage
 constexpr int kSegment = 1024;  // ids looked through at once
 constexpr int kList = 2 * kSegment;  // rows of an expert gathered for its passes
 constexpr int kPrefetch = 1024; // bytes of a row hinted to the L2 cache
+// CTAs that run at once, two on each of a B200's SMs. A constant, since
+// tq_linear_workspace, which follows the same rules, asks no GPU.
+constexpr int kPlaces = 2 * 148;
 constexpr int kTopR = 246;  // R at most: NaN (255) lies outside of its range
-constexpr int kPlaces = 2 * 148;  // CTAs that run at once
 
 struct RowArgs {
   const uint8_t *codes, *scales;  // weights (of expert 0)
@@ -90,24 +92,6 @@ struct RowPlan {
   static constexpr int kBody = kRingBytes > kPart ? kRingBytes : kPart;
   static constexpr int kSmem = kBody + kXBufs * kXBuf;
 };
-
-__device__ __forceinline__ uint32_t max_mag8(const uint4 &w) {
-  const uint32_t m = __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
-                              __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
-  return max(m >> 16, m & 0xFFFFu);
-}
-
-// max_mag8 over the finite values.
-__device__ __noinline__ uint32_t max_finite8(uint4 w) {
-  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t a = (v[i >> 1] >> (16 * (i & 1))) & 0x7FFFu;
-    if (a < 0x7F80u) m = max(m, a);
-  }
-  return m;
-}
 
 __device__ __forceinline__ uint32_t scaled_h2(uint32_t w, float s) {
   uint32_t r;

@@ -31,25 +31,6 @@
 namespace tq {
 namespace {
 
-// Largest magnitude (bf16 bits) of the 8 values of a 16-byte word.
-__device__ __forceinline__ uint32_t max_mag8(const uint4 &w) {
-  const uint32_t m = __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
-                              __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
-  return max(m >> 16, m & 0xFFFFu);
-}
-
-// The same over the finite values, one by one.
-__device__ __noinline__ uint32_t max_finite8(uint4 w) {
-  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t a = (v[i >> 1] >> (16 * (i & 1))) & 0x7FFFu;
-    if (a < 0x7F80u) m = max(m, a);
-  }
-  return m;
-}
-
 __device__ __forceinline__ float bf16_lo(uint32_t w) {
   return __uint_as_float(w << 16);
 }

@@ -1,4 +1,4 @@
-// Shared by the row products with 4-bit weights (tq_f4_linear.cu).
+// Instructions and small helpers of the row kernel (tq_f4_linear.cu).
 #pragma once
 
 #include "tq_f4.cuh"
