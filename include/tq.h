@@ -284,8 +284,8 @@ tq_status tq_unpack(const tq_weights *w, void *W_bf16_out, int32_t *dev_status,
  * for values of at least 2^-15 of the largest of their block (32 or 16
  * columns), and else at most 2^-23 of that, or 2^-40 of the row's largest if
  * that is more. Elsewhere d is 0 down to 2^-31 of the row's largest value, and
- * else at most 2^-39 of that; MX4 block scales more than 2^131 below the
- * largest of their row count as 2^131 below.
+ * else at most 2^-39 of that; MX4 blocks more than 2^100 below the largest
+ * block of their row that has any weight count as up to 2^-100 of it.
  * Format A reads: a row's codes and scales are fetched in whole 16-byte
  * blocks, from the block holding the first byte to the block holding the
  * last. A 16-byte block never crosses a page, so these reads stay in mapped

@@ -17,9 +17,10 @@
 //        exponent that this part of the row has met. A block above that moves
 //        R to its own exponent, and the sums are scaled down; a stage with a
 //        block below it multiplies its codes block by block, as they are, and
-//        applies 2^(E - R + 5) to the fp32 sums. Blocks of zero codes may carry
-//        any scale and do neither. Blocks below 2^-131 of the row's largest
-//        count as if they lay there.
+//        applies 2^(E - R + 5), at least 2^-126, to the fp32 sums. Blocks of
+//        zero codes may carry any scale and do neither; R starts as a guess,
+//        the largest scale of the first stage, and falls too while the sums
+//        are 0.
 //   x    bf16 has 8 significant bits, fp16 11 but a short range: x is held
 //        as x 2^(14 - X) with X the exponent of the largest value of its row
 //        so far, exact down to 2^(X - 31), off by at most 2^(X - 39) below.
@@ -432,8 +433,14 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
               }
               now = max(now, __shfl_xor_sync(0xFFFFFFFFu, now, 1));
               now = max(now, __shfl_xor_sync(0xFFFFFFFFu, now, 2));
-              // (with no sums yet R may fall as well)
-              now = st > 0 && now <= was + 8 ? was : min(max(now, 0), kTopR);
+              // with no sums yet R may fall as well
+              bool some = false;
+#pragma unroll
+              for (int c = 0; c < kTiles; ++c)
+                some |= acc[c][2 * r] != 0.0f || acc[c][2 * r + 1] != 0.0f;
+              const uint32_t sums = __ballot_sync(0xFFFFFFFFu, some);
+              some = (sums >> (lane & 28) & 15u) != 0;
+              now = now < 0 || (some && now <= was + 8) ? was : min(now, kTopR);
               const uint32_t nans = __ballot_sync(0xFFFFFFFFu, nan);
               // a NaN scale makes the row NaN, whatever the codes
               const bool gone = (nans >> (lane & 28) & 15u) != 0;

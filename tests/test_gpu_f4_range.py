@@ -96,6 +96,21 @@ def test_zero_block_under_large_scale(k, low, zero):
 
 
 @pytest.mark.parametrize("k", KS)
+@pytest.mark.parametrize("low,zero", [(126, 254), (20, 254), (1, 200)])
+def test_zero_blocks_before_the_first_weight(k, low, zero):
+    """Nothing but zero codes under a large scale for hundreds of columns."""
+    n, E = 70, 4
+    codes, scales = exact_package(MX4, n * E, k, 2)
+    scales = (scales.int() + low - 126).to(torch.uint8)
+    for j in list(range(8)) + list(range(16, 24)):
+        codes[:, 32 * j:32 * j + 32] &= 8
+        scales[:, j] = zero
+    s = 2.0 ** (100 if low < 126 else 0)
+    every_path(MX4, codes, scales, None,
+               lambda b: (integers(b, k, b) * s).bfloat16(), n, "zero blocks")
+
+
+@pytest.mark.parametrize("k", KS)
 @pytest.mark.parametrize("down", [28, 60, 110])
 def test_small_blocks_count(k, down):
     """Blocks far below the row's largest keep their values: x is 0 where the
