@@ -320,6 +320,7 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
                  (i - b * (NT - rows) * (P::kXPitch / 16)) * 16,
              make_uint4(0, 0, 0, 0));  // rows that are not there
     }
+    if (tid >= rows && tid < NT) s_fac[0][tid] = s_fac[1][tid] = 1.0f;
     int any = 0;
     if constexpr (P::kXBufs == 2) {
       publish(0);
@@ -433,11 +434,14 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
               }
               now = max(now, __shfl_xor_sync(0xFFFFFFFFu, now, 1));
               now = max(now, __shfl_xor_sync(0xFFFFFFFFu, now, 2));
-              // with no sums yet R may fall as well
+              // with no sums yet (NaN and Inf have no scale) R may fall as well
               bool some = false;
 #pragma unroll
-              for (int c = 0; c < kTiles; ++c)
-                some |= acc[c][2 * r] != 0.0f || acc[c][2 * r + 1] != 0.0f;
+              for (int c = 0; c < 2 * kTiles; ++c) {
+                const uint32_t u =
+                    __float_as_uint(acc[c / 2][2 * r + c % 2]) << 1;
+                some |= u - 1u < 0xFEFFFFFFu;
+              }
               const uint32_t sums = __ballot_sync(0xFFFFFFFFu, some);
               some = (sums >> (lane & 28) & 15u) != 0;
               now = now < 0 || (some && now <= was + 8) ? was : min(now, kTopR);

@@ -106,8 +106,12 @@ def test_zero_blocks_before_the_first_weight(k, low, zero):
         codes[:, 32 * j:32 * j + 32] &= 8
         scales[:, j] = zero
     s = 2.0 ** (100 if low < 126 else 0)
-    every_path(MX4, codes, scales, None,
-               lambda b: (integers(b, k, b) * s).bfloat16(), n, "zero blocks")
+
+    def x_of(b):
+        x = (integers(b, k, b) * s).bfloat16()
+        x[b // 2, 5] = float("nan")  # only this row
+        return x
+    every_path(MX4, codes, scales, None, x_of, n, "zero blocks")
 
 
 @pytest.mark.parametrize("k", KS)
