@@ -279,6 +279,7 @@ class Weights:
         # calls through ctypes take several times as long)
         self.device = device
         self.shape = (desc.n_rows, desc.k_cols)
+        self.count = desc.n_rows * desc.k_cols
         self._workspaces = {}
 
     def workspace(self, batch):
@@ -433,18 +434,18 @@ def tq_encode_b(W, ladder, zeta, rows_per_scale, codes_out, rho_out,
 
 
 def tq_unpack(w: Weights, out, dev_status=None, stream=None, check=True):
-    if w.device is not None:
-        n, k = w.shape
-        dev = w.device
+    dev = w.device
+    if dev is not None:
         if not (dev >= 0 and dev == _current_device() and
-                _f4_plain(out, torch.bfloat16, dev, n * k)):
-            _f4_operands(w, ((out, _BF16, 1, 0, n * k),), "tq_unpack")
+                _f4_plain(out, torch.bfloat16, dev, w.count)):
+            _f4_operands(w, ((out, _BF16, 1, 0, w.count),), "tq_unpack")
             if not (isinstance(out, int) or out.is_contiguous()):
                 raise TqError(TQ_ERR_INVALID_ARG, "tq_unpack: not dense")
         if dev_status is not None:
             _f4_status(dev_status, dev, "tq_unpack: dev_status")
     st = _lib.tq_unpack(w.ref, _ptr(out), _ptr(dev_status),
-                        _stream(stream, w.device))
+                        _raw_stream(dev) if stream is None and dev is not None
+                        else _stream(stream))
     if check:
         _check(st, "tq_unpack")
     return st
@@ -563,7 +564,7 @@ def tq_quantize_f4(W, fmt, codes_out, scales_out, tensor_scale=None,
     written."""
     n, k = W.shape
     dev = _f4_device(W, "tq_quantize_f4: W")
-    if not _f4_plain(W, torch.bfloat16, dev, 0):
+    if W.dtype is not torch.bfloat16 or not W.is_contiguous():
         _f4_tensor(W, _BF16, dev, "tq_quantize_f4: W")
     blocks = n * k // F4_BLOCK.get(fmt, 16)
     if not (_f4_plain(codes_out, torch.uint8, dev, n * k // 2) and
@@ -579,7 +580,7 @@ def tq_quantize_f4(W, fmt, codes_out, scales_out, tensor_scale=None,
         _f4_status(dev_status, dev, "tq_quantize_f4: dev_status")
     st = _lib.tq_quantize_f4(W.data_ptr(), n, k, _rows(W), fmt,
                              codes_out.data_ptr(), scales_out.data_ptr(),
-                             _ptr(tensor_scale), int(bool(scale_given)),
+                             _ptr(tensor_scale), 1 if scale_given else 0,
                              _ptr(dev_status), _stream(stream, dev))
     if check:
         _check(st, "tq_quantize_f4")
