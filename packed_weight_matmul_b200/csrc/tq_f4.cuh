@@ -156,10 +156,10 @@ cudaError_t digits_f4(const WeightsView &w, const __nv_bfloat16 *x,
 // rows each: all of them, but fewer where the CTAs of the passes find room next
 // to one another, K split as far as it goes. A pass of 8 rows takes about half
 // the time of one of 32 and a quarter of one of 64. Without and with that (us):
-// 1003 x 4128 at 16, 32 rows 8.8, 12.0 and 8.4, 8.9; 2048 x 2048 at 32 rows
-// 10.3 and 6.3; 198 rows over 4 experts of 111 x 576 20.7 and 8.7. Fewer rows
-// at the price of the split of K did not pay (4096 x 4096, 20 rows: 11.9, with
-// 16 instead of 32 rows per pass 16.0).
+// 1003 x 4128 at 32 rows 12.0 and 9.4; 2048 x 8192 at 32 rows 17.3 and 12.6;
+// 2048 x 2048 at 32 rows 9.1 and 6.7; 198 rows over 4 experts of 111 x 576 22
+// and 8. Fewer rows at the price of the split of K did not pay (4096 x 4096, 20
+// rows: 11.9, with 16 instead of 32 rows per pass 16.0).
 int rows_per_pass_f4(const WeightsView &w, int64_t copies, int64_t rows);
 
 // Clusters of `ks` CTAs that are resident together; 0: not known.

@@ -13,10 +13,10 @@
 // Bound by the codes' way from HBM: an MMA of 64 k takes 41 to 64 cycles for
 // 8192 weights, 2 to 3 times the rate at which HBM delivers them. A digit
 // costs 3 lane instructions per value of x and CTA, so a pass takes 4 bf16
-// rows (packed ones: 32 or 64). MX4, 8192 x 5376: 1 row 10.0 us, 16 packed rows 8.9 us
-// (HBM alone 3.6; 5 us are start-up and the sum over the cluster); 21504 x
-// 5376, 1 row: 16.5 us, 3.7 TB/s; 64 rows over 128 experts of 768 x 2048: 18
-// us.
+// rows (packed ones: 32 or 64). MX4, 8192 x 5376: 1 row 10.0 us, 16 packed
+// rows 8.7 us (HBM alone 3.6; 5 us are start-up and the sum over the cluster);
+// 21504 x 5376, 1 row: 16.8 us, 3.7 TB/s; 64 rows over 128 experts of 768 x
+// 2048: 18 us.
 //
 // One CTA per 128 weight rows and slice of K, two CTAs per SM (one starts up
 // or ends while the other streams), the slices of a tile in a cluster that

@@ -6,8 +6,9 @@
 // scales [8 rows][k/block], the rows' exponents and their flags for NaN / Inf.
 // One block per row and 2048 columns; each finds the row's largest magnitude
 // itself (the row is in the L2 cache) and turns 8 values per thread into 8
-// words of codes. Bound by arithmetic, about 30 lane instructions per value:
-// 64 x 5376 takes 4 us beside the 26 us of the product.
+// words of codes. Bound by arithmetic, 59 lane instructions per value by the
+// profiler: 64 x 5376 takes 6 us by itself, of the 40 us of a product with
+// 21504 weight rows.
 #include "tq_f4_digits.cuh"
 
 namespace tq {
@@ -108,17 +109,17 @@ __global__ void __launch_bounds__(256)
 }  // namespace
 
 // 0 where the plain kernels do as well. Measured (us; plain, digits):
-//   MX4  21504 x 5376 batch 4: 23, 16.5; 16: 43, 23; 64: 113, 40
-//        5376 x 21504 batch 4: 28, 20.6; 16: 33, 32; 32: 50, 35.5
-//        8192 x 5376 batch 4: 13.5, 11; 4096 x 4096 batch 8: 7.4, 9.4; 32:
-//        12.8, 11.6; 48: 17.8, 11.9; 2048 x 8192 batch 16: 10, 15; 32: 12.6,
-//        15.4
-//   NV4  21504 x 5376 batch 4: 29, 20; 16: 42, 28; 64: 107, 56
-//        8192 x 5376 batch 4: 12.0, 12.8; 16: 15.8, 15.1; 32: 23.5, 18
-//        5376 x 21504 batch 4: 22.7, 23.5; 16: 32, 37.5; 32: 48, 40
-//        2048 x 21504 batch 16: 19, 37; 32: 25, 36
-//        1000 x 4000 batch 64: 9.3, 14.5; 130: 19.6, 15.9
-//        128 x 512 batch 64: 4.2, 6.6; 300: 4.5, 7.2
+//   MX4  21504 x 5376 batch 4: 24, 18; 16: 43, 26; 64: 120, 40
+//        5376 x 21504 batch 4: 28, 21.6; 16: 33, 33; 32: 48, 36
+//        8192 x 5376 batch 4: 14.5, 12.2; 4096 x 4096 batch 8: 7.9, 9.7; 32:
+//        12.6, 12.2; 48: 17.5, 12.6; 2048 x 8192 batch 16: 10.3, 16; 32: 12.6,
+//        16
+//   NV4  21504 x 5376 batch 4: 29, 21; 16: 42, 29; 64: 117, 42
+//        8192 x 5376 batch 4: 12.7, 13.6; 16: 16.4, 16.1; 32: 24, 18
+//        5376 x 21504 batch 4: 23, 25; 16: 32, 39; 24: 45, 39; 32: 48, 41
+//        2048 x 21504 batch 16: 20, 37; 32: 25, 37
+//        1000 x 4000 batch 64: 9.3, 15.5; 130: 18.2, 16.5
+//        128 x 512 batch 64: 4.6, 7.3; 300: 4.8, 7.9
 // The second launch costs 4 us, and long rows of x cost more digits for the
 // same weights. The plain kernel slows down past 16 and again past 32 rows
 // unless it has room for passes of 8 or 16 next to one another; the product

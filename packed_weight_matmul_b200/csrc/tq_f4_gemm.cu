@@ -151,10 +151,11 @@ __device__ __forceinline__ uint32_t bf16_pair(uint32_t lo, uint32_t hi) {
   return *reinterpret_cast<const uint32_t *>(&p);
 }
 
-// Arrive on the barrier at this CTA's address `bar` in the pair's first CTA.
-// Relaxed: what it announces (bytes of completed tensor copies, completed
-// tensor-memory stores) is read by MMAs, not by loads that a release would
-// order, and this thread has waited for all of it.
+// Arrive on the barrier at this CTA's address `bar` in the pair's first CTA,
+// when a warp has read its part of the accumulator. Relaxed: nothing was written
+// that the other side reads. The loads from tensor memory are over
+// (tcgen05.wait::ld) and the fence before the arrival keeps them before it; a
+// release would wait for the stores of y too.
 __device__ __forceinline__ void arrive_leader(uint32_t bar) {
   uint32_t remote;
   asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(remote) : "r"(bar));
@@ -253,7 +254,7 @@ __global__ void __launch_bounds__(Plan<FMT, NT, CG>::kThreads, 1)
         }
       }
     }
-    if (rank == 0) {  // the whole warp, see mma_scaled
+    if (rank == 0) {  // the whole warp, see mma_stage
       uint32_t it = 0, done = 0;
       bool ok = true, here = false;
       for (int t = group; t < tiles && ok; t += groups, ++done) {
@@ -560,9 +561,9 @@ __global__ void __launch_bounds__(Plan<FMT, NT, CG>::kThreads, 1)
       // Chunks past the batch are left out; the branch also keeps a chunk's
       // arithmetic behind its load (without it every column stayed in 32 bits
       // until the end and was spilled: 4900 cycles for the 128 columns of a
-      // warp instead of 1150). As many columns as 64 registers hold are read first, so that the next
-      // tile can start while they are stored: all of them as bf16 pairs (two
-      // columns of this lane's row), 64 in fp32.
+      // warp instead of 1150). As many columns as 64 registers hold are read
+      // first, so that the next tile can start while they are stored: all of
+      // them as bf16 pairs (two columns of this lane's row), 64 in fp32.
       uint32_t h[kCols / 2] = {};
       if (args.digits.exps != nullptr) {
         const DigitArgs &D = args.digits;

@@ -5,9 +5,10 @@
 // for bf16 x (tq_linear) and for rows of x that pick their matrix
 // (tq_linear_experts_f4).
 // Meant to be bound by the codes' way from HBM (0.53 bytes per weight), which
-// leaves about 3 lane instructions for a weight; at 2.3 (counted) issue slots
-// and start-up bind first. NV4, 5376 x 21504, 4 rows: 22.3 us, 2.9 TB/s; 128
-// experts of 768 x 2048, 500 rows: 42 to 46 us; 1003 x 4128, 13 rows: 8.2 us.
+// leaves about 3 lane instructions for a weight. The profiler counts 3.0 (NV4,
+// 5376 x 21504, 4 rows) and 3.4 (128 experts of 768 x 2048, 500 rows), start
+// and end among them, so issue slots and start-up bind first: 22.1 us, 2.9
+// TB/s, and 45 us; 1003 x 4128, 13 rows: 8.0 us.
 //
 // Arithmetic. Codes become fp16 pairs by one conversion instruction each, are
 // multiplied by their block's scale in fp16 (exact, see below) and go as the
@@ -156,7 +157,7 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
   // Hint the L2 cache with this warp's codes, so that they are on their way
   // while the kernel before finishes: lane r takes row r of the slice. Not for
   // experts, most of whose CTAs start long after that kernel's end: 500 rows
-  // over 128 experts of 768 x 2048 (NV4) 46 us with it, 42 us without.
+  // over 128 experts of 768 x 2048 (NV4) 50 us with it, 46 us without.
   if (a.ids == nullptr && lane <= last && count > 0) {
     const int64_t from = (int64_t)st0 * (kStageK / 2);
     const int64_t to = (int64_t)st1 * (kStageK / 2);
@@ -530,8 +531,8 @@ __global__ void __launch_bounds__(RowPlan<FMT, NT>::kThreads,
         }
         // The tensor core cuts its sums instead of rounding them, so a stage
         // has sums of its own, which are added to the others with rounding.
-        // NV4, 5376 x 21504: 1.2e-7 off instead of 1.2e-6, in the same time at
-        // 4 and 12 rows, in 55 instead of 51 us at 24. 64 rows have not the
+        // NV4, 5376 x 21504: 1.2e-7 off instead of 1.2e-6, in the same time up
+        // to 16 rows, in 44.6 instead of 43.3 us at 24. 64 rows have not the
         // registers: there the sums are those of half a stage and four column
         // tiles at a time, with the half's weights decoded before (83 instead
         // of 76 us; with a stage's sums of all tiles spilled 85, with one tile
@@ -858,10 +859,10 @@ int rows_per_pass_f4(const WeightsView &w, int64_t copies, int64_t rows) {
 cudaError_t linear_f4_bf16(const WeightsView &w, const __nv_bfloat16 *x,
                            int64_t batch, int64_t ldx, float *y, int64_t ldy,
                            cudaStream_t stream) {
-  // Up to 3 (MX4: 4) rows the digits of x cost less than decoding the weights:
-  // 21504 x 5376 (MX4) at 1, 2, 4, 8 rows 16.5, 18, 23, 36 us there against
-  // 25, 26, 27, 29 us here; 5376 x 21504 (NV4) at 1, 2, 4 rows 18.7, 22, 28
-  // against 24, 24.5, 25.6 us.
+  // Up to 3 (MX4: 4) rows the digits of x cost less than decoding the weights,
+  // but for long rows of x: 21504 x 5376 (MX4) at 1, 2, 4, 8 rows 17.0, 18.8,
+  // 23.7, 35.7 us there against 28.4, 28.7, 30.2, 32.3 us here; 5376 x 21504
+  // (NV4) at 1, 2, 4 rows 21.4, 23.8, 28.8 against 21.9, 22.0, 23.3 us.
   if (batch <= (w.format == TQ_FMT_MX4 ? 4 : 3) && decode_f4_supported(w, 1))
     return decode_f4_bf16(w, x, batch, ldx, y, ldy, stream);
   RowArgs a = weight_args(w);
@@ -890,8 +891,9 @@ cudaError_t launch_linear_experts_f4(const WeightsView &w, int n_experts,
                                      const __nv_bfloat16 *x, int64_t ldx,
                                      float *y, int64_t ldy, int32_t *status,
                                      cudaStream_t stream) {
-  // The same trade: 64 rows over 128 experts of 768 x 2048 (MX4) 22 us there
-  // against 25 us here, 500 rows (NV4) 66 against 46 us.
+  // The same trade: 64 rows over 128 experts of 768 x 2048 (MX4) 18.5 us there
+  // against 24.1 us here, 257 rows 37.8 against 35.8 us, 500 rows (NV4) 59
+  // against 46 us.
   if (tokens <= n_experts && decode_f4_supported(w, n_experts))
     return decode_f4_experts(w, n_experts, ids, tokens, x, ldx, y, ldy, status,
                              stream);
@@ -907,15 +909,14 @@ cudaError_t launch_linear_experts_f4(const WeightsView &w, int n_experts,
   // Experts that get rows at all, and the rows of one: room for twice the mean.
   // With room for four times the mean fewer experts need a second pass, but
   // every pass is wider: 128 experts of 768 x 2048 (MX4) at 257, 500, 1024
-  // rows 49, 55, 74 us against 44, 48, 59 us; the other way round only where
-  // all tiles run at once and one expert's second pass is the tail (32 experts
-  // of 1024 x 4096 at 256 rows: 48 us against 55 us).
+  // rows 43, 49.5, 74 us against 36, 46.5, 55 us, 32 experts of 1024 x 4096 at
+  // 256 rows 47 against 34 us.
   const int64_t used = tokens < n_experts ? tokens : n_experts;
   const int64_t most = 2 * ((tokens + n_experts - 1) / n_experts);
   const int nt = rows_per_pass_f4(w, used, most);
   // CTAs that share an expert's passes: all of twice the mean where the passes
   // were cut for it, else what the mean needs (768 x 2048, 8 experts, 300 rows:
-  // 19 us, with one for each pass of twice the mean 28 us).
+  // 18 us, with one for each pass of twice the mean 27 us).
   const int64_t room = kPlaces / (used * ((w.n + 127) / 128));
   int64_t z = nt < 64 && nt < most / 2 ? (most + nt - 1) / nt
                                        : (most / 2 + nt - 1) / nt;
